@@ -7,3 +7,7 @@ from .sgmv import (  # noqa: F401
     sgmv_expand, sgmv_lora_add, sgmv_shrink, sgmv_status_string, sgmv_workspace_bytes,
     build_segments_device, lora_add_pool, sgmv_build_segments_device, sgmv_lora_add_pool,
 )
+from .grouped import (  # noqa: F401
+    RowGroups, group_matmul, group_matmul_dw, group_matmul_dx, group_rows,
+)
+from .mx import MxTensor, mx_dequantize, mx_matmul, mx_quantize  # noqa: F401

@@ -81,6 +81,22 @@ SIGNATURES["sgmv_build_segments_ranked"] = (ctypes.c_int, [_p, _i32, _i32, _p, _
 SIGNATURES["sgmv_lora_add_ranked"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _p, _p, _p, _p,
                                                      _i32, _p, _i32, _i32, _i32, _p, _sz])
 
+# products grouped by row ids, and weights in microscaled 4-bit floating point
+SIGNATURES["sgmv_group_rows"] = (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p])
+SIGNATURES["sgmv_group_matmul"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _i32, _p, _i64,
+                                                  _p, _p, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_group_matmul_dx"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _p, _i64, _p,
+                                                     _p, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_group_matmul_dw"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _i32, _p,
+                                                     _i64, _p, _p, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_mx_quantize"] = (ctypes.c_int, [_p, _i32, _p, _p, _p, _i64, _i64, _i32])
+SIGNATURES["sgmv_mx_dequantize"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i64, _i32])
+SIGNATURES["sgmv_mx_matmul"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _i32, _p, _p, _p,
+                                               _p, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_mx_matmul_quantized"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i32, _p,
+                                                         _p, _p, _p, _i32, _i32, _i32, _i32])
+MAX_GROUPS = 1024
+
 _LIB = None
 _PATH = LIB_PATH
 

@@ -1,0 +1,201 @@
+// Rows grouped by an id, and the products of each group's rows with its own weight: forward,
+// gradient of the rows, gradient of the weights.
+#include <type_traits>
+
+#include "sgmv_simple.h"
+
+using namespace sgmv_dev;
+using namespace sgmv_host;
+
+namespace {
+
+// ------------------------------------------------------------------------------------
+// group tables: a stable counting sort by one workgroup
+// ------------------------------------------------------------------------------------
+// Bin G takes the rows of no group.  Each wavefront owns a contiguous run of rows (a multiple
+// of 64).  It counts them per bin in LDS, the counts are summed over (bin, wavefront) in that
+// order, and each wavefront then places its rows 64 at a time: a row's place is its bin's next
+// free one plus the number of lower lanes of the same bin, found by one ballot per bit of the
+// bin number.  All counts are integers, so the tables do not depend on timing.  One workgroup
+// bounds this by its own latency (about 64 rows per wavefront and 0.2 us), which the products
+// it precedes hide many times over; several workgroups would need a second launch.
+constexpr int kBinSlots = 8 * (kMaxGroups + 1) + 8;  // 16 wavefronts up to 512 groups, 8 above
+inline int group_waves(int G) { return 16 * (G + 1) <= kBinSlots ? 16 : 8; }
+
+__global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restrict__ ids, int32_t n,
+                                                          int32_t G, int32_t* __restrict__ perm,
+                                                          int32_t* __restrict__ starts) {
+  __shared__ int bins[kBinSlots];  // [wavefront][G + 1]
+  __shared__ int sums[16];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, waves = blockDim.x >> 6;
+  const int B = G + 1;
+  for (int i = tid; i < waves * B; i += blockDim.x) bins[i] = 0;
+  __syncthreads();
+  const int run = ((n + waves - 1) / waves + 63) & ~63;
+  const int lo = min(n, w * run), hi = min(n, lo + run);
+  int* mine = bins + w * B;
+  auto bin_of = [&](int i) {
+    const int id = i < hi ? ids[i] : 0;
+    return static_cast<uint32_t>(id) < static_cast<uint32_t>(G) ? id : G;
+  };
+  for (int i = lo + lane; i < hi; i += 64) atomicAdd(&mine[bin_of(i)], 1);
+  __syncthreads();
+  // exclusive sums over bins, then over a bin's wavefronts
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    int total = 0;
+    if (b < B)
+      for (int v = 0; v < waves; ++v) total += bins[v * B + b];
+    const int incl = wave_scan(total);
+    if (lane == 63) sums[w] = incl;
+    __syncthreads();
+    int at = carry + incl - total;
+    for (int v = 0; v < w; ++v) at += sums[v];
+    for (int v = 0; v < waves; ++v) carry += sums[v];
+    if (b < B) {
+      starts[b] = at;
+      for (int v = 0; v < waves; ++v) {
+        const int c = bins[v * B + b];
+        bins[v * B + b] = at;
+        at += c;
+      }
+    }
+    __syncthreads();
+  }
+  const int bits = 32 - __builtin_clz(static_cast<uint32_t>(G));
+  volatile int* next = mine;
+  for (int i0 = lo; i0 < hi; i0 += 64) {
+    const int i = i0 + lane;
+    const bool in = i < hi;
+    const int b = bin_of(i);
+    uint64_t same = __ballot(in);
+    for (int k = 0; k < bits; ++k) {
+      const uint64_t set = __ballot((b >> k) & 1);
+      same &= (b >> k) & 1 ? set : ~set;
+    }
+    if (in) {
+      const int below = __popcll(same & ((uint64_t(1) << lane) - 1));
+      const int base = next[b];
+      perm[base + below] = i;
+      // the bin's last lane moves its next free place on, after every lane read it (LDS
+      // accesses of one wavefront keep their order)
+      if ((same >> lane) == 1) next[b] = base + below + 1;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
+  if (stride < static_cast<int64_t>(h_in) * h_out) return SGMV_ERR_SHAPE;
+  return stride % 8 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
+}
+
+template <Form RF, Form CF, int MODE>
+hipError_t launch_simple(int32_t dtype, int64_t grid, hipStream_t s, const SimpleArgs& A) {
+  if (dtype == SGMV_F16)
+    simple_kernel<SGMV_F16, RF, CF, MODE><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
+  else
+    simple_kernel<SGMV_BF16, RF, CF, MODE><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n, int32_t n_groups,
+                               int32_t* perm, int32_t* starts) {
+  if (n < 0 || n_groups < 1) return SGMV_ERR_SHAPE;
+  if (n_groups > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
+  if (!starts || (n > 0 && (!ids || !perm))) return SGMV_ERR_NULL;
+  if (int st = check_device()) return st;
+  group_rows_kernel<<<1, 64 * group_waves(n_groups), 0, stream>>>(ids, n, n_groups, perm, starts);
+  return hip_status(hipGetLastError());
+}
+
+extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                                 const void* x, int64_t ld_x, int32_t share, const void* W,
+                                 int64_t W_stride, const int32_t* starts, const int32_t* perm,
+                                 int32_t n, int32_t n_groups, int32_t h_in, int32_t h_out) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_groups(n, n_groups, share, starts, perm)) || (st = check_dim(h_in, ld_x)) ||
+      (st = check_dim(h_out, ld_y)) || (st = check_weights(W_stride, h_in, h_out)))
+    return st;
+  if (n == 0) return SGMV_OK;
+  if (!y || !x || !W) return SGMV_ERR_NULL;
+  if (!aligned16(y) || !aligned16(x) || !aligned16(W)) return SGMV_ERR_ALIGNMENT;
+  const size_t y_bytes = matrix_bytes(n, ld_y, h_out);
+  if (ranges_overlap(y, y_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
+      ranges_overlap(y, y_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
+    return SGMV_ERR_ALIAS;
+  const int64_t grid = max_row_tiles(n, n_groups, starts, 64) * ((h_out + 63) / 64);
+  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
+  SimpleArgs A{};
+  A.T = {starts, perm, n, n_groups};
+  A.share = share_of(share);
+  A.r = static_cast<const uint16_t*>(x);
+  A.c = static_cast<const uint16_t*>(W);
+  A.out = static_cast<uint16_t*>(y);
+  A.ld_r = ld_x, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = W_stride;
+  A.cols = h_out, A.depth = h_in;
+  return hip_status(launch_simple<kAlong, kAlong, 0>(dtype, grid, stream, A));
+}
+
+extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
+                                    const void* dy, int64_t ld_dy, const void* W, int64_t W_stride,
+                                    const int32_t* starts, const int32_t* perm, int32_t n,
+                                    int32_t n_groups, int32_t h_in, int32_t h_out) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_groups(n, n_groups, 1, starts, perm)) || (st = check_dim(h_in, ld_dx)) ||
+      (st = check_dim(h_out, ld_dy)) || (st = check_weights(W_stride, h_in, h_out)))
+    return st;
+  if (n == 0) return SGMV_OK;
+  if (!dx || !dy || !W) return SGMV_ERR_NULL;
+  if (!aligned16(dx) || !aligned16(dy) || !aligned16(W)) return SGMV_ERR_ALIGNMENT;
+  const size_t dx_bytes = matrix_bytes(n, ld_dx, h_in);
+  if (ranges_overlap(dx, dx_bytes, dy, matrix_bytes(n, ld_dy, h_out)) ||
+      ranges_overlap(dx, dx_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
+    return SGMV_ERR_ALIAS;
+  const int64_t grid = max_row_tiles(n, n_groups, starts, 64) * ((h_in + 63) / 64);
+  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
+  SimpleArgs A{};
+  A.T = {starts, perm, n, n_groups};
+  A.r = static_cast<const uint16_t*>(dy);
+  A.c = static_cast<const uint16_t*>(W);
+  A.out = static_cast<uint16_t*>(dx);
+  A.ld_r = ld_dy, A.ld_c = h_in, A.ld_out = ld_dx, A.c_stride = W_stride;
+  A.cols = h_in, A.depth = h_out;
+  return hip_status(launch_simple<kAlong, kAcross, 0>(dtype, grid, stream, A));
+}
+
+extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,
+                                    const void* x, int64_t ld_x, int32_t share, const void* dy,
+                                    int64_t ld_dy, const int32_t* starts, const int32_t* perm,
+                                    int32_t n, int32_t n_groups, int32_t h_in, int32_t h_out) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_groups(n, n_groups, share, starts, perm)) || (st = check_dim(h_in, ld_x)) ||
+      (st = check_dim(h_out, ld_dy)) || (st = check_weights(dW_stride, h_in, h_out)))
+    return st;
+  if (!dW || (n > 0 && (!x || !dy))) return SGMV_ERR_NULL;
+  if (!aligned16(dW) || (n > 0 && (!aligned16(x) || !aligned16(dy)))) return SGMV_ERR_ALIGNMENT;
+  const size_t dw_bytes = pool_bytes16(n_groups, dW_stride, int64_t(h_in) * h_out);
+  if (n > 0 && (ranges_overlap(dW, dw_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
+                ranges_overlap(dW, dw_bytes, dy, matrix_bytes(n, ld_dy, h_out))))
+    return SGMV_ERR_ALIAS;
+  const int64_t grid = static_cast<int64_t>(n_groups) * ((h_out + 63) / 64) * ((h_in + 63) / 64);
+  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
+  SimpleArgs A{};
+  A.T = {starts, perm, n, n_groups};
+  A.share = share_of(share);
+  A.r = static_cast<const uint16_t*>(dy);
+  A.c = static_cast<const uint16_t*>(x);
+  A.out = static_cast<uint16_t*>(dW);
+  A.ld_r = ld_dy, A.ld_c = ld_x, A.ld_out = h_in, A.out_stride = dW_stride;
+  A.rows = h_out, A.cols = h_in;
+  return hip_status(launch_simple<kAcross, kAcross, 1>(dtype, grid, stream, A));
+}

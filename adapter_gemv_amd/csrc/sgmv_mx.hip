@@ -1,0 +1,212 @@
+// Microscaled 4-bit floating point: 16-bit values to the format and back, and products with
+// weights (and rows) held in it.
+#include <type_traits>
+
+#include "sgmv_simple.h"
+
+using namespace sgmv_dev;
+using namespace sgmv_host;
+
+namespace {
+
+constexpr int kMxBlock = 32;
+
+// Four lanes to a block of 32, 8 elements (16 bytes) each: a wavefront reads 1 KB and writes
+// 256 bytes of codes in one access each.  The block's largest magnitude is the largest of the
+// magnitudes' bit patterns (a NaN's pattern is above infinity's, so neither is lost).
+template <int DT>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(uint32_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales,
+                                                          const uint16_t* __restrict__ x, int64_t ld,
+                                                          int64_t rows, int32_t h) {
+  const int64_t per_row = h / 8, total = rows * per_row;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;  // h / 8 is a multiple of 4: a block's lanes leave together
+  const int64_t row = i / per_row, at = i % per_row;
+  const uint4 v = ld16(x + row * ld + 8 * at);
+  float f[8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f[e] = elem<DT>(v, e);
+    top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+  }
+  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 1)));
+  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 2)));
+  const bool finite = top < 0x7f800000u;
+  const int e = top == 0 ? -127 : max(__builtin_amdgcn_frexp_expf(__uint_as_float(top)) - 3, -127);
+  uint32_t word = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float a = ldexpf(fabsf(f[k]), -e);
+    uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.f);
+    c |= (__float_as_uint(f[k]) >> 28) & 8u;
+    word |= c << (4 * k);
+  }
+  codes[i] = finite ? word : 0u;
+  if ((i & 3) == 0) scales[i / 4] = static_cast<uint8_t>(finite ? e + 127 : 255);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(uint16_t* __restrict__ y, int64_t ld,
+                                                            const uint32_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales,
+                                                            int64_t rows, int32_t h) {
+  const int64_t per_row = h / 8, total = rows * per_row;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int64_t row = i / per_row, at = i % per_row;
+  const uint32_t w = codes[i];
+  const float s = mx_scale(scales[i / 4]);
+  uint32_t out[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = (w >> (8 * k)) & 15, b = (w >> (8 * k + 4)) & 15;
+    const uint32_t fa = kFp4F16[a & 7] | ((a & 8) << 12), fb = kFp4F16[b & 7] | ((b & 8) << 12);
+    out[k] = Elem<DT>::pack(Elem<SGMV_F16>::lo(fa) * s, Elem<SGMV_F16>::lo(fb) * s);
+  }
+  store_words<4>(y + row * ld + 8 * at, out);
+}
+
+inline int check_mx_rows(int64_t rows, int32_t h, int64_t ld) {
+  if (rows < 0 || rows > (int64_t(1) << 40) / h) return SGMV_ERR_SHAPE;
+  if (h % kMxBlock != 0 || ld % 8 != 0) return SGMV_ERR_ALIGNMENT;
+  return h < kMxBlock || h > kMaxDim || ld < h ? SGMV_ERR_SHAPE : SGMV_OK;
+}
+
+inline size_t rows_bytes16(int64_t rows, int64_t ld, int32_t h) {
+  return rows <= 0 ? 0 : 2 * (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + static_cast<size_t>(h));
+}
+
+}  // namespace
+
+extern "C" int sgmv_mx_quantize(hipStream_t stream, int32_t dtype, void* codes, void* scales,
+                                const void* x, int64_t ld_x, int64_t rows, int32_t h) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  if (h < 1) return SGMV_ERR_SHAPE;
+  if (int st = check_mx_rows(rows, h, ld_x)) return st;
+  if (rows == 0) return SGMV_OK;
+  if (!codes || !scales || !x) return SGMV_ERR_NULL;
+  if (!aligned16(codes) || !aligned8(scales) || !aligned16(x)) return SGMV_ERR_ALIGNMENT;
+  const size_t elems = static_cast<size_t>(rows) * h, x_bytes = rows_bytes16(rows, ld_x, h);
+  if (ranges_overlap(codes, elems / 2, x, x_bytes) || ranges_overlap(scales, elems / 32, x, x_bytes) ||
+      ranges_overlap(codes, elems / 2, scales, elems / 32))
+    return SGMV_ERR_ALIAS;
+  if (int st = check_device()) return st;
+  const uint32_t grid = static_cast<uint32_t>((elems / 8 + 255) / 256);
+  auto* c = static_cast<uint32_t*>(codes);
+  auto* s = static_cast<uint8_t*>(scales);
+  auto* p = static_cast<const uint16_t*>(x);
+  if (dtype == SGMV_F16) mx_quantize_kernel<SGMV_F16><<<grid, 256, 0, stream>>>(c, s, p, ld_x, rows, h);
+  else mx_quantize_kernel<SGMV_BF16><<<grid, 256, 0, stream>>>(c, s, p, ld_x, rows, h);
+  return hip_status(hipGetLastError());
+}
+
+extern "C" int sgmv_mx_dequantize(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                                  const void* codes, const void* scales, int64_t rows, int32_t h) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  if (h < 1) return SGMV_ERR_SHAPE;
+  if (int st = check_mx_rows(rows, h, ld_y)) return st;
+  if (rows == 0) return SGMV_OK;
+  if (!codes || !scales || !y) return SGMV_ERR_NULL;
+  if (!aligned16(codes) || !aligned8(scales) || !aligned16(y)) return SGMV_ERR_ALIGNMENT;
+  const size_t elems = static_cast<size_t>(rows) * h, y_bytes = rows_bytes16(rows, ld_y, h);
+  if (ranges_overlap(codes, elems / 2, y, y_bytes) || ranges_overlap(scales, elems / 32, y, y_bytes))
+    return SGMV_ERR_ALIAS;
+  if (int st = check_device()) return st;
+  const uint32_t grid = static_cast<uint32_t>((elems / 8 + 255) / 256);
+  auto* c = static_cast<const uint32_t*>(codes);
+  auto* s = static_cast<const uint8_t*>(scales);
+  auto* p = static_cast<uint16_t*>(y);
+  if (dtype == SGMV_F16) mx_dequantize_kernel<SGMV_F16><<<grid, 256, 0, stream>>>(p, ld_y, c, s, rows, h);
+  else mx_dequantize_kernel<SGMV_BF16><<<grid, 256, 0, stream>>>(p, ld_y, c, s, rows, h);
+  return hip_status(hipGetLastError());
+}
+
+namespace {
+
+// the checks that both products share; 0 when fine (n may be 0)
+inline int check_mx_product(int32_t dtype, const void* y, int64_t ld_y, int32_t share,
+                            const void* W_codes, const void* W_scales, const int32_t* starts,
+                            const int32_t* perm, int32_t n, int32_t G, int32_t h_in, int32_t h_out,
+                            int64_t* grid) {
+  if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_groups(n, G, share, starts, perm)) || (st = check_dim(h_out, ld_y))) return st;
+  if (h_in < 1) return SGMV_ERR_SHAPE;
+  if ((st = check_mx_rows(0, h_in, h_in))) return st;
+  if (n == 0) return SGMV_OK;
+  if (!y || !W_codes || !W_scales) return SGMV_ERR_NULL;
+  if (!aligned16(y) || !aligned16(W_codes) || !aligned8(W_scales)) return SGMV_ERR_ALIGNMENT;
+  const size_t y_bytes = matrix_bytes(n, ld_y, h_out), elems = static_cast<size_t>(G) * h_in * h_out;
+  if (ranges_overlap(y, y_bytes, W_codes, elems / 2) || ranges_overlap(y, y_bytes, W_scales, elems / 32))
+    return SGMV_ERR_ALIAS;
+  *grid = max_row_tiles(n, G, starts, 64) * ((h_out + 63) / 64);
+  return *grid > INT32_MAX ? SGMV_ERR_SHAPE : SGMV_OK;
+}
+
+template <Form RF>
+hipError_t launch_mx(int32_t dtype, int64_t grid, hipStream_t s, const SimpleArgs& A) {
+  if (dtype == SGMV_F16)
+    simple_kernel<SGMV_F16, RF, kCodes, 0><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
+  else
+    simple_kernel<SGMV_BF16, RF, kCodes, 0><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                              const void* x, int64_t ld_x, int32_t share, const void* W_codes,
+                              const void* W_scales, const int32_t* starts, const int32_t* perm,
+                              int32_t n, int32_t n_groups, int32_t h_in, int32_t h_out) {
+  int64_t grid = 0;
+  int st = check_mx_product(dtype, y, ld_y, share, W_codes, W_scales, starts, perm, n, n_groups, h_in,
+                            h_out, &grid);
+  if (st || (st = check_dim(h_in, ld_x))) return st;
+  if (n == 0) return SGMV_OK;
+  if (!x) return SGMV_ERR_NULL;
+  if (!aligned16(x)) return SGMV_ERR_ALIGNMENT;
+  if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
+    return SGMV_ERR_ALIAS;
+  if ((st = check_device())) return st;
+  SimpleArgs A{};
+  A.T = {starts, perm, n, n_groups};
+  A.share = share_of(share);
+  A.r = static_cast<const uint16_t*>(x);
+  A.c = static_cast<const uint16_t*>(W_codes);
+  A.c_scale = static_cast<const uint8_t*>(W_scales);
+  A.out = static_cast<uint16_t*>(y);
+  A.ld_r = ld_x, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = static_cast<int64_t>(h_in) * h_out;
+  A.cols = h_out, A.depth = h_in;
+  return hip_status(launch_mx<kAlong>(dtype, grid, stream, A));
+}
+
+extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                                        const void* x_codes, const void* x_scales, int32_t share,
+                                        const void* W_codes, const void* W_scales,
+                                        const int32_t* starts, const int32_t* perm, int32_t n,
+                                        int32_t n_groups, int32_t h_in, int32_t h_out) {
+  int64_t grid = 0;
+  int st = check_mx_product(dtype, y, ld_y, share, W_codes, W_scales, starts, perm, n, n_groups, h_in,
+                            h_out, &grid);
+  if (st || n == 0) return st;
+  if (!x_codes || !x_scales) return SGMV_ERR_NULL;
+  if (!aligned16(x_codes) || !aligned8(x_scales)) return SGMV_ERR_ALIGNMENT;
+  const size_t y_bytes = matrix_bytes(n, ld_y, h_out);
+  const size_t elems = static_cast<size_t>(shared_rows(n, share)) * h_in;
+  if (ranges_overlap(y, y_bytes, x_codes, elems / 2) || ranges_overlap(y, y_bytes, x_scales, elems / 32))
+    return SGMV_ERR_ALIAS;
+  if ((st = check_device())) return st;
+  SimpleArgs A{};
+  A.T = {starts, perm, n, n_groups};
+  A.share = share_of(share);
+  A.r = static_cast<const uint16_t*>(x_codes);
+  A.c = static_cast<const uint16_t*>(W_codes);
+  A.r_scale = static_cast<const uint8_t*>(x_scales);
+  A.c_scale = static_cast<const uint8_t*>(W_scales);
+  A.out = static_cast<uint16_t*>(y);
+  A.ld_r = h_in, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = static_cast<int64_t>(h_in) * h_out;
+  A.cols = h_out, A.depth = h_in;
+  return hip_status(launch_mx<kCodes>(dtype, grid, stream, A));
+}

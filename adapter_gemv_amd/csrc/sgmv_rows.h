@@ -1,0 +1,137 @@
+// Group tables on the device and the host checks shared by the grouped products
+// (sgmv_group.hip) and the products with microscaled 4-bit weights (sgmv_mx.hip).
+#pragma once
+
+#include "sgmv_checks.h"
+#include "sgmv_device.h"
+
+namespace sgmv_dev {
+
+// Rows of a batch by group: rows perm[starts[g] .. starts[g+1]) belong to group g, rows
+// perm[starts[G] .. n) to none.  starts == nullptr: one group of n rows in caller order.
+struct RowTab {
+  const int32_t* starts;
+  const int32_t* perm;
+  int32_t n, G;
+  __device__ int row(int j) const { return perm ? perm[j] : j; }
+};
+
+// i / share for 0 <= i < 2^31 / share by a multiplication: m = ceil(2^32 / share) is off by
+// less than share / 2^32, so the product's high word is exact below 2^32 / share (the host
+// checks n * share)
+struct Share {
+  uint32_t m;  // 0 for share == 1
+  __device__ int div(int i) const { return m ? static_cast<int>(__umulhi(i, m)) : i; }
+};
+
+// `rows` positions of the tables from `row0` on, all of group g (G: of no group)
+struct RowTile {
+  int g, row0, rows;
+};
+
+// inclusive sum over the lanes of a wavefront
+__device__ inline int wave_scan(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int u = __shfl_up(v, d);
+    if ((threadIdx.x & 63) >= d) v += u;
+  }
+  return v;
+}
+
+// How many tiles of at most BM rows the groups make (the rows of no group are tiled too,
+// behind them, if `rest`): wave-uniform, every lane of the wave takes part.
+__device__ inline int lane_tiles(const RowTab& T, int g, int BM, bool rest, int* first, int* len) {
+  const int last = rest ? T.G : T.G - 1;
+  int a = 0, b = 0;
+  if (g <= last) {
+    a = T.starts[g];
+    b = g < T.G ? T.starts[g + 1] : T.n;
+  }
+  *first = a;
+  *len = b - a;
+  return (b - a + BM - 1) / BM;
+}
+
+// The tiles of all groups, counted and found by one wavefront: 64 groups at a time, one to a
+// lane.  `count` is their number; find(m) is the m-th (0 <= m < count).  Both are uniform.
+struct TileList {
+  RowTab T;
+  int BM;
+  bool rest;
+  int count;
+  int first, len, incl;  // this lane's group of the first 64, and its inclusive tile count
+
+  __device__ TileList(const RowTab& t, int bm, bool with_rest) : T(t), BM(bm), rest(with_rest) {
+    if (!T.starts) {
+      count = (T.n + BM - 1) / BM;
+      return;
+    }
+    const int lane = threadIdx.x & 63;
+    incl = wave_scan(lane_tiles(T, lane, BM, rest, &first, &len));
+    count = __builtin_amdgcn_readlane(incl, 63);
+    for (int g0 = 64; g0 <= T.G; g0 += 64) {
+      int f, l;
+      count += __builtin_amdgcn_readlane(wave_scan(lane_tiles(T, g0 + lane, BM, rest, &f, &l)), 63);
+    }
+  }
+
+  __device__ RowTile find(int m) const {
+    if (!T.starts) return {0, m * BM, min(BM, T.n - m * BM)};
+    const int lane = threadIdx.x & 63;
+    int f = first, l = len, in = incl, before = 0, g0 = 0;
+    for (;;) {
+      const uint64_t past = __ballot(before + in > m);
+      if (past) {
+        const int who = __builtin_ctzll(past);
+        const int gf = __builtin_amdgcn_readlane(f, who), gl = __builtin_amdgcn_readlane(l, who);
+        const int tiles = (gl + BM - 1) / BM;
+        const int at = m - (before + __builtin_amdgcn_readlane(in, who) - tiles);
+        return {g0 + who, gf + at * BM, min(BM, gl - at * BM)};
+      }
+      before += __builtin_amdgcn_readlane(in, 63);
+      g0 += 64;
+      if (g0 > T.G) return {T.G, 0, 0};
+      in = wave_scan(lane_tiles(T, g0 + lane, BM, rest, &f, &l));
+    }
+  }
+};
+
+}  // namespace sgmv_dev
+
+namespace sgmv_host {
+
+constexpr int kMaxGroups = SGMV_MAX_GROUPS;
+
+inline sgmv_dev::Share share_of(int32_t share) {
+  return {share == 1 ? 0u
+                     : static_cast<uint32_t>(((uint64_t(1) << 32) + share - 1) / static_cast<uint64_t>(share))};
+}
+
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// tables and group count of a grouped call; 0 when fine (n may be 0)
+inline int check_groups(int32_t n, int32_t G, int32_t share, const int32_t* starts,
+                        const int32_t* perm) {
+  if (n < 0 || G < 1 || share < 1) return SGMV_ERR_SHAPE;
+  if (G > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n) * share > INT32_MAX) return SGMV_ERR_SHAPE;
+  if (!starts && G != 1) return SGMV_ERR_NULL;
+  if (n > 0 && (starts == nullptr) != (perm == nullptr)) return SGMV_ERR_NULL;
+  return SGMV_OK;
+}
+
+// rows of x that n rows sharing it read
+inline int32_t shared_rows(int32_t n, int32_t share) { return (n + share - 1) / share; }
+
+// at most this many row tiles of BM rows in the groups and behind them
+inline int64_t max_row_tiles(int32_t n, int32_t G, bool grouped, int BM) {
+  const int64_t full = n / BM + (grouped ? G + 1 : 1);
+  return full < n ? full : n;
+}
+
+inline size_t pool_bytes16(int32_t G, int64_t stride, int64_t elems) {
+  return 2 * (static_cast<size_t>(G - 1) * static_cast<size_t>(stride) + static_cast<size_t>(elems));
+}
+
+}  // namespace sgmv_host

@@ -422,6 +422,112 @@ int sgmv_lora_add_host_ids_noalloc(hipStream_t stream, int32_t dtype, void* y, i
                                    const void* B_pool, int64_t B_stride, int32_t n_adapters,
                                    int32_t h_in, int32_t h_out, int32_t r, float scale);
 
+/*
+ * Products grouped by an id on each row, for the backbone products that one library GEMM
+ * does not serve: expert layers, where row i goes through its own expert's whole weight.
+ * With g = ids[i] in [0, n_groups):
+ *
+ *     y[i, :]     = x[i / share, :] @ W[g]^T                        (sgmv_group_matmul)
+ *     dx[i, :]    = dy[i, :] @ W[g]                                 (sgmv_group_matmul_dx)
+ *     dW[g]       = sum over the rows i of g: dy[i, :]^T x[i / share, :]   (..._dw)
+ *
+ * W[g] is [h_out, h_in] row-major (the nn.Linear layout), groups W_stride elements apart
+ * (W_stride >= h_out * h_in, a multiple of 8).  `share` consecutive rows read one row of
+ * x (a token that goes to `share` experts): x has ceil(n / share) rows, y, dx and dy have
+ * n; dx is per row, so a shared x's gradient is the sum of its rows' dx.  Types, strides
+ * and alignment are as for the LoRA calls: everything SGMV_F16 or everything SGMV_BF16,
+ * h_in, h_out and row strides multiples of 8, bases 16-byte aligned.  Sums are float32 and
+ * each output is rounded once, to nearest even.  Outputs are overwritten.
+ *
+ * The rows of each group are listed by the tables of sgmv_group_rows: row perm[j],
+ * starts[g] <= j < starts[g+1], belongs to group g, and rows perm[starts[n_groups] .. n)
+ * belong to none (their id lies outside [0, n_groups): an expert held elsewhere, padding).
+ * A row of no group gets zeros in y and dx and adds nothing to any dW; a group without
+ * rows gets a dW of zeros.  starts == NULL (with perm == NULL and n_groups == 1) makes all
+ * n rows one group in caller order: a dense product.
+ *
+ * These calls need no workspace.  Their errors are those of the other calls: SGMV_ERR_SHAPE
+ * (also for share < 1 and for products of more than 2^31 - 1 tiles), SGMV_ERR_ALIGNMENT,
+ * SGMV_ERR_NULL, SGMV_ERR_UNSUPPORTED (dtype; n_groups above SGMV_MAX_GROUPS),
+ * SGMV_ERR_ALIAS (an output overlaps an input), SGMV_ERR_HIP.
+ */
+#define SGMV_MAX_GROUPS 1024
+
+/*
+ * Group tables of n rows (device, one launch, no host work that depends on the ids).  The
+ * sort is stable: rows of one group keep their caller order, so results do not depend on
+ * timing.
+ *   ids     device int32[n]; ids outside [0, n_groups) put a row in no group
+ *   perm    device int32[n] out
+ *   starts  device int32[n_groups + 1] out; starts[0] = 0, starts[n_groups] = the number
+ *           of rows that belong to a group
+ * 1 <= n_groups <= SGMV_MAX_GROUPS.  n == 0 still writes starts (zeros).
+ */
+int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n, int32_t n_groups,
+                    int32_t* perm, int32_t* starts);
+
+int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* x,
+                      int64_t ld_x, int32_t share, const void* W, int64_t W_stride,
+                      const int32_t* starts, const int32_t* perm, int32_t n, int32_t n_groups,
+                      int32_t h_in, int32_t h_out);
+
+int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
+                         const void* dy, int64_t ld_dy, const void* W, int64_t W_stride,
+                         const int32_t* starts, const int32_t* perm, int32_t n,
+                         int32_t n_groups, int32_t h_in, int32_t h_out);
+
+/* dW has groups dW_stride elements apart, each [h_out, h_in]; every group is written, also
+ * with n == 0. */
+int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,
+                         const void* x, int64_t ld_x, int32_t share, const void* dy,
+                         int64_t ld_dy, const int32_t* starts, const int32_t* perm, int32_t n,
+                         int32_t n_groups, int32_t h_in, int32_t h_out);
+
+/*
+ * Microscaled 4-bit floating point ("MX": one copy of a backbone weight in 17/32 of a byte
+ * per element).  A row of h elements (h a multiple of 32) is h / 32 blocks; a block has one
+ * scale 2^(b - 127), stored as the byte b, and 32 elements of one sign, two exponent and
+ * one mantissa bit: codes 0..7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and code + 8 for the
+ * negative.  codes: uint8 [rows, h / 2], the element at an even place in the low half of
+ * its byte; scales: uint8 [rows, h / 32]; both dense, codes 16-byte and scales 8-byte
+ * aligned.  b == 255 stands for NaN: every element of the block is NaN.
+ *
+ * sgmv_mx_quantize takes SGMV_F16 or SGMV_BF16 rows to the format: the scale is
+ * 2^(floor(log2(m)) - 2) of the block's largest magnitude m, not below 2^-127 (b = 0 for a
+ * block of zeros); an element divided by it is rounded to the nearest value, ties to the
+ * even code, and what passes 6 becomes 6.  A block that holds an infinity or a NaN gets
+ * b = 255 and codes 0.
+ * sgmv_mx_dequantize writes the values the codes stand for, rounded once to dtype.
+ */
+int sgmv_mx_quantize(hipStream_t stream, int32_t dtype, void* codes, void* scales,
+                     const void* x, int64_t ld_x, int64_t rows, int32_t h);
+
+int sgmv_mx_dequantize(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                       const void* codes, const void* scales, int64_t rows, int32_t h);
+
+/*
+ * sgmv_group_matmul with weights in MX: y[i, :] = x[i / share, :] @ W[g]^T with W[g] the
+ * values of W_codes + g * h_out * h_in / 2 and W_scales + g * h_out * h_in / 32 (groups
+ * dense, blocks along h_in, h_in a multiple of 32).  x is dtype, as y: the form for decode
+ * batches, which stream the weight, and for prompts that keep 16-bit activations.
+ * Elements and scales take part exactly (no weight is rounded on its way to the product);
+ * sums are float32.
+ */
+int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* x,
+                   int64_t ld_x, int32_t share, const void* W_codes, const void* W_scales,
+                   const int32_t* starts, const int32_t* perm, int32_t n, int32_t n_groups,
+                   int32_t h_in, int32_t h_out);
+
+/*
+ * The same with x in MX too (x_codes [rows of x, h_in / 2], x_scales [rows of x, h_in / 32],
+ * as sgmv_mx_quantize writes them); dtype is y's.
+ */
+int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                             const void* x_codes, const void* x_scales, int32_t share,
+                             const void* W_codes, const void* W_scales, const int32_t* starts,
+                             const int32_t* perm, int32_t n, int32_t n_groups, int32_t h_in,
+                             int32_t h_out);
+
 #ifdef __cplusplus
 }
 #endif
