@@ -2,10 +2,14 @@
 // gradient of the rows, gradient of the weights.
 #include <type_traits>
 
-#include "sgmv_simple.h"
+#include "sgmv_tile.h"
 
 using namespace sgmv_dev;
 using namespace sgmv_host;
+
+#ifndef TILE_BIG
+#define TILE_BIG 192
+#endif
 
 namespace {
 
@@ -91,13 +95,42 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
   return stride % 8 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
 }
 
-template <Form RF, Form CF, int MODE>
-hipError_t launch_simple(int32_t dtype, int64_t grid, hipStream_t s, const SimpleArgs& A) {
-  if (dtype == SGMV_F16)
-    simple_kernel<SGMV_F16, RF, CF, MODE><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
-  else
-    simple_kernel<SGMV_BF16, RF, CF, MODE><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
+template <int DT, Form RF, Form CF, bool DW, int BR, int BC, int WR, int WC>
+hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
+  if (tiles > INT32_MAX - 8 * 1024) return hipErrorInvalidValue;
+  const uint32_t grid = static_cast<uint32_t>((tiles + kTileXcds - 1) / kTileXcds * kTileXcds);
+  tile_kernel<DT, RF, CF, DW, BR, BC, WR, WC><<<grid, 64 * WR * WC, 0, s>>>(A);
   return hipGetLastError();
+}
+
+// y and dx: row tiles of every group (and of the rows of none) times column tiles
+template <Form CF>
+hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
+  const int avg = A.T.n / A.T.G;
+  const auto tiles = [&](int BR, int BC) {
+    return max_row_tiles(A.T.n, A.T.G, A.T.starts, BR) * ((A.cols + BC - 1) / BC);
+  };
+  const bool f16 = dtype == SGMV_F16;
+  if (avg >= TILE_BIG) {
+    return f16 ? launch_tile<SGMV_F16, kAlong, CF, false, 256, 256, 2, 4>(s, tiles(256, 256), A)
+               : launch_tile<SGMV_BF16, kAlong, CF, false, 256, 256, 2, 4>(s, tiles(256, 256), A);
+  }
+  return f16 ? launch_tile<SGMV_F16, kAlong, CF, false, 128, 128, 2, 2>(s, tiles(128, 128), A)
+             : launch_tile<SGMV_BF16, kAlong, CF, false, 128, 128, 2, 2>(s, tiles(128, 128), A);
+}
+
+hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
+  const auto tiles = [&](int B) {
+    const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
+    return (t + kTileXcds - 1) / kTileXcds * kTileXcds * A.T.G;
+  };
+  const bool f16 = dtype == SGMV_F16;
+  if (A.T.n / A.T.G >= TILE_BIG) {
+    return f16 ? launch_tile<SGMV_F16, kAcross, kAcross, true, 256, 256, 2, 4>(s, tiles(256), A)
+               : launch_tile<SGMV_BF16, kAcross, kAcross, true, 256, 256, 2, 4>(s, tiles(256), A);
+  }
+  return f16 ? launch_tile<SGMV_F16, kAcross, kAcross, true, 128, 128, 2, 2>(s, tiles(128), A)
+             : launch_tile<SGMV_BF16, kAcross, kAcross, true, 128, 128, 2, 2>(s, tiles(128), A);
 }
 
 }  // namespace
@@ -128,18 +161,17 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
   if (ranges_overlap(y, y_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
       ranges_overlap(y, y_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
-  const int64_t grid = max_row_tiles(n, n_groups, starts, 64) * ((h_out + 63) / 64);
-  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
-  SimpleArgs A{};
+  TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);
-  A.r = static_cast<const uint16_t*>(x);
-  A.c = static_cast<const uint16_t*>(W);
+  A.r = static_cast<const char*>(x);
+  A.c = static_cast<const char*>(W);
   A.out = static_cast<uint16_t*>(y);
-  A.ld_r = ld_x, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = W_stride;
-  A.cols = h_out, A.depth = h_in;
-  return hip_status(launch_simple<kAlong, kAlong, 0>(dtype, grid, stream, A));
+  A.ld_r = 2 * ld_x, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_y, A.c_group = 2 * W_stride;
+  A.cols = h_out, A.depth = 2 * h_in;
+  return hip_status(launch_rows<kAlong>(dtype, stream, A));
 }
 
 extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
@@ -158,17 +190,16 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
   if (ranges_overlap(dx, dx_bytes, dy, matrix_bytes(n, ld_dy, h_out)) ||
       ranges_overlap(dx, dx_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
-  const int64_t grid = max_row_tiles(n, n_groups, starts, 64) * ((h_in + 63) / 64);
-  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if (!tiles_fit(n, n_groups, starts, h_in)) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
-  SimpleArgs A{};
+  TileArgs A{};
   A.T = {starts, perm, n, n_groups};
-  A.r = static_cast<const uint16_t*>(dy);
-  A.c = static_cast<const uint16_t*>(W);
+  A.r = static_cast<const char*>(dy);
+  A.c = static_cast<const char*>(W);
   A.out = static_cast<uint16_t*>(dx);
-  A.ld_r = ld_dy, A.ld_c = h_in, A.ld_out = ld_dx, A.c_stride = W_stride;
+  A.ld_r = 2 * ld_dy, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_dx, A.c_group = 2 * W_stride;
   A.cols = h_in, A.depth = h_out;
-  return hip_status(launch_simple<kAlong, kAcross, 0>(dtype, grid, stream, A));
+  return hip_status(launch_rows<kAcross>(dtype, stream, A));
 }
 
 extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,
@@ -186,16 +217,16 @@ extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW,
   if (n > 0 && (ranges_overlap(dW, dw_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
                 ranges_overlap(dW, dw_bytes, dy, matrix_bytes(n, ld_dy, h_out))))
     return SGMV_ERR_ALIAS;
-  const int64_t grid = static_cast<int64_t>(n_groups) * ((h_out + 63) / 64) * ((h_in + 63) / 64);
-  if (grid > INT32_MAX) return SGMV_ERR_SHAPE;
+  if (static_cast<int64_t>(n_groups) * (h_out / 64 + 8) * (h_in / 64 + 8) > INT32_MAX)
+    return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
-  SimpleArgs A{};
+  TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);
-  A.r = static_cast<const uint16_t*>(dy);
-  A.c = static_cast<const uint16_t*>(x);
+  A.r = static_cast<const char*>(dy);
+  A.c = static_cast<const char*>(x);
   A.out = static_cast<uint16_t*>(dW);
-  A.ld_r = ld_dy, A.ld_c = ld_x, A.ld_out = h_in, A.out_stride = dW_stride;
+  A.ld_r = 2 * ld_dy, A.ld_c = 2 * ld_x, A.ld_out = h_in, A.out_group = dW_stride;
   A.rows = h_out, A.cols = h_in;
-  return hip_status(launch_simple<kAcross, kAcross, 1>(dtype, grid, stream, A));
+  return hip_status(launch_dw(dtype, stream, A));
 }
