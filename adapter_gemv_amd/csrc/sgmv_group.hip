@@ -2,6 +2,7 @@
 // gradient of the rows, gradient of the weights.
 #include <type_traits>
 
+#include "sgmv_skinny.h"
 #include "sgmv_tile.h"
 
 using namespace sgmv_dev;
@@ -95,6 +96,9 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
   return stride % 8 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
 }
 
+// rows per group, on average, below which the streaming kernel runs
+constexpr int kSkinnyMost = 24;
+
 template <int DT, Form RF, Form CF, bool DW, int BR, int BC, int WR, int WC>
 hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
   if (tiles > INT32_MAX - 8 * 1024) return hipErrorInvalidValue;
@@ -163,6 +167,18 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
     return SGMV_ERR_ALIAS;
   if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
+  if (n / n_groups < kSkinnyMost) {
+    SkinnyArgs S{};
+    S.T = {starts, perm, n, n_groups};
+    S.share = share_of(share);
+    S.x = static_cast<const uint16_t*>(x);
+    S.w = static_cast<const char*>(W);
+    S.y = static_cast<uint16_t*>(y);
+    S.ld_x = ld_x, S.ld_y = ld_y, S.w_group = 2 * W_stride, S.h_in = h_in, S.h_out = h_out;
+    const int64_t tiles = max_row_tiles(n, n_groups, starts, kSkinnyRows);
+    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, false>(stream, S, tiles)
+                                        : launch_skinny<SGMV_BF16, false>(stream, S, tiles));
+  }
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);

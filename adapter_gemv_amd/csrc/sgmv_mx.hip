@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "sgmv_simple.h"
+#include "sgmv_skinny.h"
 
 using namespace sgmv_dev;
 using namespace sgmv_host;
@@ -170,6 +171,20 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
+  if (n / n_groups < 1000000) {
+    SkinnyArgs S{};
+    S.T = {starts, perm, n, n_groups};
+    S.share = share_of(share);
+    S.x = static_cast<const uint16_t*>(x);
+    S.w = static_cast<const char*>(W_codes);
+    S.scales = static_cast<const uint8_t*>(W_scales);
+    S.y = static_cast<uint16_t*>(y);
+    S.ld_x = ld_x, S.ld_y = ld_y, S.w_group = static_cast<int64_t>(h_in) * h_out / 2;
+    S.h_in = h_in, S.h_out = h_out;
+    const int64_t tiles = max_row_tiles(n, n_groups, starts, kSkinnyRows);
+    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, true>(stream, S, tiles)
+                                        : launch_skinny<SGMV_BF16, true>(stream, S, tiles));
+  }
   SimpleArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);

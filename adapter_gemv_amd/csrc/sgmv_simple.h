@@ -2,7 +2,7 @@
 // operands staged through registers into LDS 32 contracted elements at a time.
 #pragma once
 
-#include "sgmv_rows.h"
+#include "sgmv_skinny.h"
 
 namespace sgmv_dev {
 
@@ -22,10 +22,6 @@ struct SimpleArgs {
   int64_t ld_r, ld_c, ld_out, c_stride, out_stride;
   int32_t rows, cols, depth;       // dW only: rows; columns of the output; contracted length
 };
-
-__device__ inline float mx_scale(uint32_t b) {
-  return b == 255 ? __builtin_nanf("") : (b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22));
-}
 
 // MODE 0: y / dx (rows gathered; a column operand per group); MODE 1: dW (contracted over rows)
 template <int DT, Form RF, Form CF, int MODE>
