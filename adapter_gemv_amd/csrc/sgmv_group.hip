@@ -8,10 +8,6 @@
 using namespace sgmv_dev;
 using namespace sgmv_host;
 
-#ifndef TILE_BIG
-#define TILE_BIG 192
-#endif
-
 namespace {
 
 // ------------------------------------------------------------------------------------
@@ -99,30 +95,6 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
 // rows per group, on average, below which the streaming kernel runs
 constexpr int kSkinnyMost = 24;
 
-template <int DT, Form RF, Form CF, bool DW, int BR, int BC, int WR, int WC>
-hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
-  if (tiles > INT32_MAX - 8 * 1024) return hipErrorInvalidValue;
-  const uint32_t grid = static_cast<uint32_t>((tiles + kTileXcds - 1) / kTileXcds * kTileXcds);
-  tile_kernel<DT, RF, CF, DW, BR, BC, WR, WC><<<grid, 64 * WR * WC, 0, s>>>(A);
-  return hipGetLastError();
-}
-
-// y and dx: row tiles of every group (and of the rows of none) times column tiles
-template <Form CF>
-hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
-  const int avg = A.T.n / A.T.G;
-  const auto tiles = [&](int BR, int BC) {
-    return max_row_tiles(A.T.n, A.T.G, A.T.starts, BR) * ((A.cols + BC - 1) / BC);
-  };
-  const bool f16 = dtype == SGMV_F16;
-  if (avg >= TILE_BIG) {
-    return f16 ? launch_tile<SGMV_F16, kAlong, CF, false, 256, 256, 2, 4>(s, tiles(256, 256), A)
-               : launch_tile<SGMV_BF16, kAlong, CF, false, 256, 256, 2, 4>(s, tiles(256, 256), A);
-  }
-  return f16 ? launch_tile<SGMV_F16, kAlong, CF, false, 128, 128, 2, 2>(s, tiles(128, 128), A)
-             : launch_tile<SGMV_BF16, kAlong, CF, false, 128, 128, 2, 2>(s, tiles(128, 128), A);
-}
-
 hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
   const auto tiles = [&](int B) {
     const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
@@ -130,11 +102,11 @@ hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
   };
   const bool f16 = dtype == SGMV_F16;
   if (A.T.n / A.T.G >= TILE_BIG) {
-    return f16 ? launch_tile<SGMV_F16, kAcross, kAcross, true, 256, 256, 2, 4>(s, tiles(256), A)
-               : launch_tile<SGMV_BF16, kAcross, kAcross, true, 256, 256, 2, 4>(s, tiles(256), A);
+    return f16 ? launch_tile<SGMV_F16, kDw, 256, 256, 2, 4>(s, tiles(256), A)
+               : launch_tile<SGMV_BF16, kDw, 256, 256, 2, 4>(s, tiles(256), A);
   }
-  return f16 ? launch_tile<SGMV_F16, kAcross, kAcross, true, 128, 128, 2, 2>(s, tiles(128), A)
-             : launch_tile<SGMV_BF16, kAcross, kAcross, true, 128, 128, 2, 2>(s, tiles(128), A);
+  return f16 ? launch_tile<SGMV_F16, kDw, 128, 128, 2, 2>(s, tiles(128), A)
+             : launch_tile<SGMV_BF16, kDw, 128, 128, 2, 2>(s, tiles(128), A);
 }
 
 }  // namespace
@@ -187,7 +159,7 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
   A.out = static_cast<uint16_t*>(y);
   A.ld_r = 2 * ld_x, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_y, A.c_group = 2 * W_stride;
   A.cols = h_out, A.depth = 2 * h_in;
-  return hip_status(launch_rows<kAlong>(dtype, stream, A));
+  return hip_status(launch_rows<kForward>(dtype, stream, A));
 }
 
 extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
@@ -215,7 +187,7 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
   A.out = static_cast<uint16_t*>(dx);
   A.ld_r = 2 * ld_dy, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_dx, A.c_group = 2 * W_stride;
   A.cols = h_in, A.depth = h_out;
-  return hip_status(launch_rows<kAcross>(dtype, stream, A));
+  return hip_status(launch_rows<kDx>(dtype, stream, A));
 }
 
 extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,

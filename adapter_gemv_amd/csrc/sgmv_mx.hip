@@ -2,8 +2,8 @@
 // weights (and rows) held in it.
 #include <type_traits>
 
-#include "sgmv_simple.h"
 #include "sgmv_skinny.h"
+#include "sgmv_tile.h"
 
 using namespace sgmv_dev;
 using namespace sgmv_host;
@@ -11,6 +11,8 @@ using namespace sgmv_host;
 namespace {
 
 constexpr int kMxBlock = 32;
+// rows per group, on average, below which the streaming kernel runs
+constexpr int kMxSkinnyMost = 48;
 
 // Four lanes to a block of 32, 8 elements (16 bytes) each: a wavefront reads 1 KB and writes
 // 256 bytes of codes in one access each.  The block's largest magnitude is the largest of the
@@ -62,9 +64,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(uint16_t* __restrict
   uint32_t out[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t a = (w >> (8 * k)) & 15, b = (w >> (8 * k + 4)) & 15;
-    const uint32_t fa = kFp4F16[a & 7] | ((a & 8) << 12), fb = kFp4F16[b & 7] | ((b & 8) << 12);
-    out[k] = Elem<DT>::pack(Elem<SGMV_F16>::lo(fa) * s, Elem<SGMV_F16>::lo(fb) * s);
+    const uint32_t e = word(mx_eight<SGMV_F16>(w, 1.f), k);
+    out[k] = Elem<DT>::pack(Elem<SGMV_F16>::lo(e) * s, Elem<SGMV_F16>::hi(e) * s);
   }
   store_words<4>(y + row * ld + 8 * at, out);
 }
@@ -129,8 +130,8 @@ namespace {
 // the checks that both products share; 0 when fine (n may be 0)
 inline int check_mx_product(int32_t dtype, const void* y, int64_t ld_y, int32_t share,
                             const void* W_codes, const void* W_scales, const int32_t* starts,
-                            const int32_t* perm, int32_t n, int32_t G, int32_t h_in, int32_t h_out,
-                            int64_t* grid) {
+                            const int32_t* perm, int32_t n, int32_t G, int32_t h_in,
+                            int32_t h_out) {
   if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
   int st;
   if ((st = check_groups(n, G, share, starts, perm)) || (st = check_dim(h_out, ld_y))) return st;
@@ -142,17 +143,7 @@ inline int check_mx_product(int32_t dtype, const void* y, int64_t ld_y, int32_t 
   const size_t y_bytes = matrix_bytes(n, ld_y, h_out), elems = static_cast<size_t>(G) * h_in * h_out;
   if (ranges_overlap(y, y_bytes, W_codes, elems / 2) || ranges_overlap(y, y_bytes, W_scales, elems / 32))
     return SGMV_ERR_ALIAS;
-  *grid = max_row_tiles(n, G, starts, 64) * ((h_out + 63) / 64);
-  return *grid > INT32_MAX ? SGMV_ERR_SHAPE : SGMV_OK;
-}
-
-template <Form RF>
-hipError_t launch_mx(int32_t dtype, int64_t grid, hipStream_t s, const SimpleArgs& A) {
-  if (dtype == SGMV_F16)
-    simple_kernel<SGMV_F16, RF, kCodes, 0><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
-  else
-    simple_kernel<SGMV_BF16, RF, kCodes, 0><<<static_cast<uint32_t>(grid), 256, 0, s>>>(A);
-  return hipGetLastError();
+  return tiles_fit(n, G, starts, h_out) ? SGMV_OK : SGMV_ERR_SHAPE;
 }
 
 }  // namespace
@@ -161,9 +152,8 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
                               const void* x, int64_t ld_x, int32_t share, const void* W_codes,
                               const void* W_scales, const int32_t* starts, const int32_t* perm,
                               int32_t n, int32_t n_groups, int32_t h_in, int32_t h_out) {
-  int64_t grid = 0;
   int st = check_mx_product(dtype, y, ld_y, share, W_codes, W_scales, starts, perm, n, n_groups, h_in,
-                            h_out, &grid);
+                            h_out);
   if (st || (st = check_dim(h_in, ld_x))) return st;
   if (n == 0) return SGMV_OK;
   if (!x) return SGMV_ERR_NULL;
@@ -171,7 +161,7 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
-  if (n / n_groups < 1000000) {
+  if (n / n_groups < kMxSkinnyMost) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -185,16 +175,17 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
     return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, true>(stream, S, tiles)
                                         : launch_skinny<SGMV_BF16, true>(stream, S, tiles));
   }
-  SimpleArgs A{};
+  TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);
-  A.r = static_cast<const uint16_t*>(x);
-  A.c = static_cast<const uint16_t*>(W_codes);
+  A.r = static_cast<const char*>(x);
+  A.c = static_cast<const char*>(W_codes);
   A.c_scale = static_cast<const uint8_t*>(W_scales);
   A.out = static_cast<uint16_t*>(y);
-  A.ld_r = ld_x, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = static_cast<int64_t>(h_in) * h_out;
-  A.cols = h_out, A.depth = h_in;
-  return hip_status(launch_mx<kAlong>(dtype, grid, stream, A));
+  A.ld_r = 2 * ld_x, A.ld_c = h_in / 2, A.ld_out = ld_y;
+  A.c_group = static_cast<int64_t>(h_in) * h_out / 2;
+  A.cols = h_out, A.depth = 2 * h_in;
+  return hip_status(launch_rows<kMxW>(dtype, stream, A));
 }
 
 extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
@@ -202,9 +193,8 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
                                         const void* W_codes, const void* W_scales,
                                         const int32_t* starts, const int32_t* perm, int32_t n,
                                         int32_t n_groups, int32_t h_in, int32_t h_out) {
-  int64_t grid = 0;
   int st = check_mx_product(dtype, y, ld_y, share, W_codes, W_scales, starts, perm, n, n_groups, h_in,
-                            h_out, &grid);
+                            h_out);
   if (st || n == 0) return st;
   if (!x_codes || !x_scales) return SGMV_ERR_NULL;
   if (!aligned16(x_codes) || !aligned8(x_scales)) return SGMV_ERR_ALIGNMENT;
@@ -213,15 +203,17 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
   if (ranges_overlap(y, y_bytes, x_codes, elems / 2) || ranges_overlap(y, y_bytes, x_scales, elems / 32))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
-  SimpleArgs A{};
+  TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);
-  A.r = static_cast<const uint16_t*>(x_codes);
-  A.c = static_cast<const uint16_t*>(W_codes);
+  A.r = static_cast<const char*>(x_codes);
+  A.c = static_cast<const char*>(W_codes);
   A.r_scale = static_cast<const uint8_t*>(x_scales);
   A.c_scale = static_cast<const uint8_t*>(W_scales);
   A.out = static_cast<uint16_t*>(y);
-  A.ld_r = h_in, A.ld_c = h_in, A.ld_out = ld_y, A.c_stride = static_cast<int64_t>(h_in) * h_out;
-  A.cols = h_out, A.depth = h_in;
-  return hip_status(launch_mx<kCodes>(dtype, grid, stream, A));
+  A.ld_r = h_in / 2, A.ld_c = h_in / 2, A.ld_out = ld_y;
+  A.c_group = static_cast<int64_t>(h_in) * h_out / 2;
+  A.cols = h_out, A.depth = h_in / 2;
+  return hip_status(h_in % 256 == 0 ? launch_rows<kMxBoth, true>(dtype, stream, A)
+                                    : launch_rows<kMxBoth, false>(dtype, stream, A));
 }

@@ -19,6 +19,15 @@
 //   kAcross: 32-byte column block p of contracted row k sits in block p ^ spread(k); the 16
 //            rows that one transposing read touches then cover the banks evenly.
 //
+// Weights in 4 bits against 16-bit rows (kMxW): a stage of a weight row is 32 bytes of codes
+// (kCodes); a lane reads 16 codes, one half for each half of the stage, and converts them with
+// their scale to the 16-bit operand, exactly in bfloat16.  For float16 rows the product runs in
+// bfloat16 too, the rows taken apart into two bfloat16 parts (8 + 3 of their 11 bits), since
+// float16 does not hold every element times its scale.
+// Both sides in 4 bits (kMxBoth): the fragments are the 16x16x128 scaled MFMA's operands, whose
+// blocks of 32 are the format's own; the scale bytes go through LDS in the order in which its
+// byte selectors take them.
+//
 // Output rows are the second MFMA operand and output columns the first, so a lane holds four
 // neighbouring columns of one row; v_permlane16_swap pairs two column tiles into eight, and
 // every store is 16 bytes.
@@ -30,12 +39,12 @@
 
 #include <type_traits>
 
-#include "sgmv_rows.h"
+#include "sgmv_skinny.h"
 
 namespace sgmv_dev {
 
-enum Form { kAlong, kAcross };
-constexpr int kMx4 = 2;  // element type of the tile product beside SGMV_F16 and SGMV_BF16
+enum Form { kAlong, kAcross, kCodes };
+enum Mode { kForward, kDx, kDw, kMxW, kMxBoth };
 
 typedef __attribute__((ext_vector_type(8))) int i32x8_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
@@ -61,7 +70,7 @@ struct TileArgs {
   RowTab T;
   Share share;
   const char *r, *c;                  // row and column operands
-  const uint8_t *r_scale, *c_scale;   // kMx4
+  const uint8_t *r_scale, *c_scale;   // kMxBoth, kMxW: dense, blocks / row as depth says
   uint16_t* out;
   int64_t ld_r, ld_c, ld_out;         // bytes between rows of r and c; elements of out
   int64_t c_group, out_group;         // bytes between groups of c; elements of out
@@ -69,22 +78,40 @@ struct TileArgs {
                                       // row (kAlong) or contracted rows (kAcross)
 };
 
-template <int DT, Form RF, Form CF, bool DW, int BR, int BC, int WR, int WC>
+template <int I, int N, class F>
+__device__ inline void tile_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    tile_for<I + 1, N>(f);
+  }
+}
+
+template <Mode M, int BR, int BC, int WR, int WC>
 struct Tile {
+  static constexpr Form RF = M == kDw ? kAcross : kAlong;
+  static constexpr Form CF = M == kDx || M == kDw ? kAcross : M == kMxW ? kCodes : kAlong;
+  static constexpr bool DW = M == kDw;
   static constexpr int NW = WR * WC, TH = 64 * NW;
   static constexpr int NR = BR / WR / 16, NC = BC / WC / 16;  // fragments of a wavefront
-  static constexpr int RI = BR / 8 / NW, CI = BC / 8 / NW;    // loads of a wavefront per stage
-  static_assert(RI * 8 * NW == BR && CI * 8 * NW == BC && NC % 2 == 0, "");
+  static constexpr int CP = M == kMxW ? 2 : 8;                // 16-byte pieces of a column's stage
+  static constexpr int RI = BR * 8 / 64 / NW, CI = BC * CP / 64 / NW;  // loads per stage
+  static_assert(RI * 64 * NW == BR * 8 && CI * 64 * NW == BC * CP && NC % 2 == 0, "");
   static_assert(NR >= NC, "column fragments are fetched one to a row step");
   static_assert(!DW || BR == BC, "dW shares its row indices between the operands");
+  static_assert(M != kMxBoth || (BR == BC && BR + BC == TH), "one thread to a row's or column's scales");
+  static_assert(M != kMxW || 2 * BC == TH, "one thread to a column's block");
 
+  // scale bytes as a lane takes them.  kMxBoth: [lane group][wavefront tile][row of 16]
+  // [fragment][half] of the rows, then of the columns; kMxW: [half][wavefront tile][row of 16]
+  // [fragment] of the columns
+  static constexpr int SC = M == kMxBoth ? 8 * BR : 0;  // where the columns' start
+  struct MxScales {
+    uint8_t b[M == kMxBoth ? 8 * (BR + BC) : M == kMxW ? 2 * BC : 16];
+  };
   struct Stage {
     uint4 r[BR * 8];
-    uint4 c[BC * 8];
-  };
-  struct Scales {  // [lane group][wavefront tile][row of 16][fragment][half stage]
-    uint8_t r[4][WR][16][NR][2];
-    uint8_t c[4][WC][16][NC][2];
+    uint4 c[BC * CP];
+    MxScales s;
   };
 
   static __device__ int spread(int B, int k) {
@@ -104,11 +131,14 @@ __device__ inline void band_order(int i, int R, int C, int* r, int* c) {
   *r = band * H + in - *c * h;
 }
 
-template <int DT, Form RF, Form CF, bool DW, int BR, int BC, int WR, int WC>
+// DT: type of the 16-bit operands and of the output.  WHOLE (kMxBoth): a row has a multiple of 8
+// blocks, so a stage's 8 scale bytes are one aligned load.
+template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
 __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
-  using C = Tile<DT, RF, CF, DW, BR, BC, WR, WC>;
+  using C = Tile<M, BR, BC, WR, WC>;
   constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI;
-  constexpr int OUT = DT;
+  constexpr Form RF = C::RF, CF = C::CF;
+  constexpr bool DW = C::DW;
   __shared__ typename C::Stage b0, b1;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
   const int wr = w / WC, wc = w % WC;
@@ -171,6 +201,10 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       const int q = (w * CI + i) * 8 + lane / 8;
       ck[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
       cp[i] = cbase + min(c0 + q, A.cols - 1) * A.ld_c + ck[i];
+    } else if constexpr (CF == kCodes) {
+      const int q = (w * CI + i) * 32 + lane / 2;
+      ck[i] = 16 * (lane & 1);
+      cp[i] = cbase + min(c0 + q, A.cols - 1) * A.ld_c + ck[i];
     } else {
       constexpr int L = BC / 8;
       ck[i] = (w * CI + i) * (64 / L) + lane / L;
@@ -178,7 +212,7 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       cp[i] = cbase + 2 * min(c0 + col, A.cols - 8) + (DW ? 0 : ck[i] * A.ld_c);
     }
   }
-  constexpr int STEP = CF == kAlong ? 128 : 64;  // of `depth`
+  constexpr int STEP = CF == kAcross ? 64 : 128;  // of `depth`
   const int nst = (depth + STEP - 1) / STEP;
 
   // dW: rows of the stage after the next one to be fetched
@@ -203,20 +237,70 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       rows_of(s + 1);
     } else {
       const int64_t rs = static_cast<int64_t>(s) * 128;
-      const int64_t cs = CF == kAlong ? rs : s * 64 * A.ld_c;
+      const int64_t cs = CF == kAlong ? rs : CF == kCodes ? rs / 4 : s * 64 * A.ld_c;
       const int left = depth - s * STEP;
-      const int rleft = CF == kAlong ? left : 2 * left;  // r lies along its rows: bytes
+      const int rleft = CF == kAcross ? 2 * left : left;  // r lies along its rows: bytes
+      const int cleft = CF == kCodes ? left / 4 : left;
 #pragma unroll
       for (int i = 0; i < RI; ++i)
         to_lds(rk[i] < rleft ? rp[i] + rs : zeros, &st.r[(w * RI + i) * 64]);
 #pragma unroll
       for (int i = 0; i < CI; ++i)
-        to_lds(ck[i] < left ? cp[i] + cs : zeros, &st.c[(w * CI + i) * 64]);
+        to_lds(ck[i] < cleft ? cp[i] + cs : zeros, &st.c[(w * CI + i) * 64]);
+    }
+  };
+  // scales: this thread's row or column of the tile, 8 bytes a stage (kMxBoth), or one block of
+  // a column, 1 byte (kMxW); fetched a stage ahead and put into LDS behind the products
+  const uint8_t* sp = nullptr;
+  int blocks = 0;       // of a row
+  int sto = 0;          // where in MxScales
+  uint32_t sv[2] = {0, 0};
+  if constexpr (M == kMxBoth) {
+    blocks = depth / 16;
+    const bool is_r = tid < BR;
+    const int q = is_r ? tid : tid - BR, N = is_r ? NR : NC;
+    sto = (is_r ? 0 : C::SC) + ((q / (16 * N)) * 16 + q % 16) * N * 2 + q / 16 % N * 2;
+    static_assert(WR * NR == WC * NC, "one distance between lane groups");
+    if (depth)
+      sp = is_r ? A.r_scale + static_cast<int64_t>(A.share.div(A.T.row(t.row0 + min(q, t.rows - 1)))) * blocks
+                : A.c_scale + (static_cast<int64_t>(t.g) * A.cols + min(c0 + q, A.cols - 1)) * blocks;
+  } else if constexpr (M == kMxW) {
+    blocks = depth / 64;
+    const int q = tid % BC, half = tid / BC;
+    sto = ((half * WC + q / (16 * NC)) * 16 + q % 16) * NC + q / 16 % NC;
+    if (depth)
+      sp = A.c_scale + (static_cast<int64_t>(t.g) * A.cols + min(c0 + q, A.cols - 1)) * blocks;
+  }
+  auto fetch_scales = [&](int s) {
+    if constexpr (M == kMxBoth && WHOLE) {
+      const u32x2_t v = *(gptr<const u32x2_t>)global_ptr(sp + 8 * min(s, blocks / 8 - 1));
+      sv[0] = v.x, sv[1] = v.y;
+    } else if constexpr (M == kMxBoth) {
+      sv[0] = sv[1] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = global_ptr(sp)[min(8 * s + i, blocks - 1)];
+        sv[i / 4] |= (8 * s + i < blocks ? b : 127u) << (8 * (i & 3));
+      }
+    } else if constexpr (M == kMxW) {
+      const int k = 2 * s + tid / BC;
+      const uint32_t b = global_ptr(sp)[min(k, blocks - 1)];
+      sv[0] = k < blocks ? b : 127u;
+    }
+  };
+  auto store_scales = [&](typename C::Stage& st) {  // no branch: see the loop below
+    if constexpr (M == kMxBoth) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint16_t*>(st.s.b + sto + k * (WR * NR * 32)) =
+            static_cast<uint16_t>(__builtin_amdgcn_perm(sv[1], sv[0], k | (4 + k) << 8));
+    } else if constexpr (M == kMxW) {
+      st.s.b[sto] = static_cast<uint8_t>(sv[0]);
     }
   };
   auto fragment = [&](auto form, auto width, const uint4* base, int tile16, int u) -> uint4 {
     if constexpr (decltype(form)::value == kAlong) {
-      return base[(tile16 * 16 + l16) * 8 + ((u * 4 + kq) ^ ((l16 >> 1) & 7))];
+      return base[(tile16 * 16 + l16) * 8 + ((M == kMxW ? kq * 2 + u : u * 4 + kq) ^ ((l16 >> 1) & 7))];
     } else {
       constexpr int B = decltype(width)::value;
       const int k = u * 32 + kq * 8 + (l16 >> 2);
@@ -242,27 +326,68 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
   // steps; the fences keep the compiler from hoisting more reads than there are registers for.
   auto stage = [&](const typename C::Stage& st, typename C::Stage& next, int s) {
     uint4 cv[2][NC], rv[2];
+    uint32_t rs[NR / 2], cs[NC / 2];
+    if constexpr (M == kMxW) {
+      uint2 codes[NC];
+      const uint8_t* from = st.s.b + (((kq >> 1) * WC + wc) * 16 + l16) * NC;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) cv[0][j] = cfrag(st, j, 0);
+      for (int j = 0; j < NC; ++j)
+        codes[j] = reinterpret_cast<const uint2*>(st.c)[((wc * NC + j) * 16 + l16) * 4 + kq];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const float f = mx_scale(from[j]);
+        cv[0][j] = mx_eight<SGMV_BF16>(codes[j].x, f);
+        cv[1][j] = mx_eight<SGMV_BF16>(codes[j].y, f);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) cv[0][j] = cfrag(st, j, 0);
+    }
+    if constexpr (M == kMxBoth) {
+      const uint32_t* r = reinterpret_cast<const uint32_t*>(st.s.b + ((kq * WR + wr) * 16 + l16) * NR * 2);
+      const uint32_t* c = reinterpret_cast<const uint32_t*>(st.s.b + C::SC + ((kq * WC + wc) * 16 + l16) * NC * 2);
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i) rs[i] = r[i];
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j) cs[j] = c[j];
+    }
     rv[0] = rfrag(st, 0, 0);
+    fetch_scales(s + 1);
     issue(next, s + 1);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < 2 * NR; ++n) {
-      const int u = n / NR, i = n % NR;
-      if (n + 1 < 2 * NR) rv[(n + 1) & 1] = rfrag(st, (n + 1) % NR, (n + 1) / NR);
-      if (u == 0 && i >= NR - NC) cv[1][i - (NR - NC)] = cfrag(st, i - (NR - NC), 1);
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[i][j] = Elem<DT>::mfma(cv[u][j], rv[n & 1], acc[i][j]);
+    tile_for<0, 2 * NR>([&](auto step) {
+      constexpr int n = decltype(step)::value, u = n / NR, i = n % NR;
+      if constexpr (n + 1 < 2 * NR) rv[(n + 1) & 1] = rfrag(st, (n + 1) % NR, (n + 1) / NR);
+      if constexpr (M != kMxW && u == 0 && i >= NR - NC) cv[1][i - (NR - NC)] = cfrag(st, i - (NR - NC), 1);
+      uint4 hi, lo;
+      if constexpr (M == kMxW && DT == SGMV_F16) f16_split(rv[n & 1], &hi, &lo);
+      tile_for<0, NC>([&](auto col) {
+        constexpr int j = decltype(col)::value;
+        if constexpr (M == kMxBoth) {
+          const uint4 a = cv[u][j], b = rv[n & 1];
+          const i32x8_t av = {int(a.x), int(a.y), int(a.z), int(a.w), 0, 0, 0, 0};
+          const i32x8_t bv = {int(b.x), int(b.y), int(b.z), int(b.w), 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              av, bv, acc[i][j], 4, 4, (j % 2) * 2 + u, cs[j / 2], (i % 2) * 2 + u, rs[i / 2]);
+        } else if constexpr (M == kMxW && DT == SGMV_F16) {
+          acc[i][j] = Elem<SGMV_BF16>::mfma(cv[u][j], hi, acc[i][j]);
+          acc[i][j] = Elem<SGMV_BF16>::mfma(cv[u][j], lo, acc[i][j]);
+        } else {
+          acc[i][j] = Elem<DT>::mfma(cv[u][j], rv[n & 1], acc[i][j]);
+        }
+      });
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
+    store_scales(next);
   };
 
   // stages in pairs, one to a buffer (an odd count's last stage, and the one fetched behind the
   // end, are zeros): no branch inside the loop, which keeps the accumulators where they are
   if (nst > 0) {
     rows_of(0);
+    fetch_scales(0);
     issue(b0, 0);
+    store_scales(b0);
     for (int s = 0; s < nst; s += 2) {
       wait_stage();
       stage(b0, b1, s);
@@ -289,7 +414,7 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
     uint16_t* to = A.out + (DW ? static_cast<int64_t>(t.g) * A.out_group : 0) + row * A.ld_out;
 #pragma unroll
     for (int j = 0; j < NC; j += 2) {
-      using E = Elem<OUT>;
+      using E = Elem<DT>;
       const f32x4_t a = acc[i][j], b = acc[i][j + 1];
       const auto lo = __builtin_amdgcn_permlane16_swap(E::pack(a[0], a[1]), E::pack(b[0], b[1]), false, false);
       const auto hi = __builtin_amdgcn_permlane16_swap(E::pack(a[2], a[3]), E::pack(b[2], b[3]), false, false);
@@ -298,6 +423,33 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       if (in && c < A.cols) store_words<4>(to + c, o);
     }
   }
+}
+
+#ifndef TILE_BIG
+#define TILE_BIG 192
+#endif
+
+template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
+hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
+  const uint32_t grid = static_cast<uint32_t>((tiles + kTileXcds - 1) / kTileXcds * kTileXcds);
+  tile_kernel<DT, M, BR, BC, WR, WC, WHOLE><<<grid, 64 * WR * WC, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+// row tiles of every group (and of the rows of none) times column tiles
+template <Mode M, bool WHOLE = true>
+hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
+  const int avg = A.T.n / A.T.G;
+  const auto tiles = [&](int BR, int BC) {
+    return sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, BR) * ((A.cols + BC - 1) / BC);
+  };
+  const bool f16 = dtype == SGMV_F16;
+  if (avg >= TILE_BIG) {
+    return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, tiles(256, 256), A)
+               : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, tiles(256, 256), A);
+  }
+  return f16 ? launch_tile<SGMV_F16, M, 128, 128, 2, 2, WHOLE>(s, tiles(128, 128), A)
+             : launch_tile<SGMV_BF16, M, 128, 128, 2, 2, WHOLE>(s, tiles(128, 128), A);
 }
 
 }  // namespace sgmv_dev
