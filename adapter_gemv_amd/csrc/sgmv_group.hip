@@ -95,18 +95,19 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
 // rows per group, on average, below which the streaming kernel runs
 constexpr int kSkinnyMost = 24;
 
+template <int DT, int B, int WR, int WC>
+hipError_t launch_dw(hipStream_t s, const TileArgs& A) {
+  const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
+  const int64_t tiles = (t + kTileXcds - 1) / kTileXcds * kTileXcds * A.T.G;
+  return A.T.perm ? launch_tile<DT, kDw, B, B, WR, WC, true>(s, tiles, A)
+                  : launch_tile<DT, kDw, B, B, WR, WC, false>(s, tiles, A);
+}
+
 hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
-  const auto tiles = [&](int B) {
-    const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
-    return (t + kTileXcds - 1) / kTileXcds * kTileXcds * A.T.G;
-  };
   const bool f16 = dtype == SGMV_F16;
-  if (A.T.n / A.T.G >= TILE_BIG) {
-    return f16 ? launch_tile<SGMV_F16, kDw, 256, 256, 2, 4>(s, tiles(256), A)
-               : launch_tile<SGMV_BF16, kDw, 256, 256, 2, 4>(s, tiles(256), A);
-  }
-  return f16 ? launch_tile<SGMV_F16, kDw, 128, 128, 2, 2>(s, tiles(128), A)
-             : launch_tile<SGMV_BF16, kDw, 128, 128, 2, 2>(s, tiles(128), A);
+  if (A.T.n / A.T.G >= TILE_BIG)
+    return f16 ? launch_dw<SGMV_F16, 256, 2, 4>(s, A) : launch_dw<SGMV_BF16, 256, 2, 4>(s, A);
+  return f16 ? launch_dw<SGMV_F16, 128, 2, 2>(s, A) : launch_dw<SGMV_BF16, 128, 2, 2>(s, A);
 }
 
 }  // namespace

@@ -20,8 +20,11 @@ struct RowTab {
 // less than share / 2^32, so the product's high word is exact below 2^32 / share (the host
 // checks n * share)
 struct Share {
-  uint32_t m;  // 0 for share == 1
+  uint32_t m;    // 0 for share == 1
+  uint32_t one;  // all bits for share == 1
   __device__ int div(int i) const { return m ? static_cast<int>(__umulhi(i, m)) : i; }
+  // the same without a branch
+  __device__ int div_any(int i) const { return static_cast<int>(__umulhi(i, m) | (i & one)); }
 };
 
 // `rows` positions of the tables from `row0` on, all of group g (G: of no group)
@@ -104,8 +107,8 @@ namespace sgmv_host {
 constexpr int kMaxGroups = SGMV_MAX_GROUPS;
 
 inline sgmv_dev::Share share_of(int32_t share) {
-  return {share == 1 ? 0u
-                     : static_cast<uint32_t>(((uint64_t(1) << 32) + share - 1) / static_cast<uint64_t>(share))};
+  if (share == 1) return {0u, ~0u};
+  return {static_cast<uint32_t>(((uint64_t(1) << 32) + share - 1) / static_cast<uint64_t>(share)), 0u};
 }
 
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }

@@ -16,8 +16,11 @@
 // belongs in its slot.
 //   kAlong:  piece c of tile row q sits in slot c ^ ((q >> 1) & 7) of the row's 8; the 16 rows
 //            of a fragment then cover all 64 banks once.
-//   kAcross: 32-byte column block p of contracted row k sits in block p ^ spread(k); the 16
-//            rows that one transposing read touches then cover the banks evenly.
+//   kAcross: one load instruction fills a slab of 1 KB with the contracted rows that no one
+//            transposing read takes together (those that differ in their place in the half
+//            stage's eight, h, or in the half, u), and slabs are 32 bytes further apart than
+//            they are long; the 16 rows of a read then lie in 16 slabs, over all banks, at
+//            constant offsets from one address per lane.
 //
 // Weights in 4 bits against 16-bit rows (kMxW): a stage of a weight row is 32 bytes of codes
 // (kCodes); a lane reads 16 codes, one half for each half of the stage, and converts them with
@@ -86,6 +89,17 @@ __device__ inline void tile_for(F&& f) {
   }
 }
 
+// kAcross, tiles of B columns: pieces of 16 bytes between slabs, contracted rows of a slab
+constexpr int kSlab = 66;
+constexpr int slab_rows(int B) { return 512 / B; }
+// the contracted row (of the stage's 64) that is row `in` of slab q
+template <int B>
+__device__ inline int slab_row(int q, int in) {
+  static_assert(B == 256 || B == 128, "");
+  return B == 256 ? (q >> 4) * 32 + ((q >> 2) & 3) * 8 + in * 4 + (q & 3)
+                  : (in >> 1) * 32 + (q >> 2) * 8 + (in & 1) * 4 + (q & 3);
+}
+
 template <Mode M, int BR, int BC, int WR, int WC>
 struct Tile {
   static constexpr Form RF = M == kDw ? kAcross : kAlong;
@@ -109,15 +123,10 @@ struct Tile {
     uint8_t b[M == kMxBoth ? 8 * (BR + BC) : M == kMxW ? 2 * BC : 16];
   };
   struct Stage {
-    uint4 r[BR * 8];
-    uint4 c[BC * CP];
+    uint4 r[RF == kAcross ? BR / 8 * kSlab : BR * 8];
+    uint4 c[CF == kAcross ? BC / 8 * kSlab : BC * CP];
     MxScales s;
   };
-
-  static __device__ int spread(int B, int k) {
-    const int j = k & 3, q = (k >> 3) & 3;
-    return B >= 256 ? j | (q << 2) : B == 128 ? j | ((q & 1) << 2) : (j >> 1) | ((q & 1) << 1);
-  }
 };
 
 constexpr int kTileXcds = 8;
@@ -131,8 +140,8 @@ __device__ inline void band_order(int i, int R, int C, int* r, int* c) {
   *r = band * H + in - *c * h;
 }
 
-// DT: type of the 16-bit operands and of the output.  WHOLE (kMxBoth): a row has a multiple of 8
-// blocks, so a stage's 8 scale bytes are one aligned load.
+// DT: type of the 16-bit operands and of the output.  WHOLE: kMxBoth, a row has a multiple of 8
+// blocks, so a stage's 8 scale bytes are one aligned load; kDw, the rows come through perm.
 template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
 __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
   using C = Tile<M, BR, BC, WR, WC>;
@@ -190,9 +199,8 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       rp[i] = A.r + j * A.ld_r + rk[i];
     } else {
       constexpr int L = BR / 8;  // lanes to a contracted row
-      rk[i] = (w * RI + i) * (64 / L) + lane / L;
-      const int p = lane % L, col = 16 * ((p >> 1) ^ C::spread(BR, rk[i])) + 8 * (p & 1);
-      rp[i] = A.r + 2 * min(r0 + col, A.rows - 8);
+      rk[i] = slab_row<BR>(w * RI + i, lane / L);
+      rp[i] = A.r + 2 * min(r0 + 8 * (lane % L), A.rows - 8);
     }
   }
 #pragma unroll
@@ -207,32 +215,35 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       cp[i] = cbase + min(c0 + q, A.cols - 1) * A.ld_c + ck[i];
     } else {
       constexpr int L = BC / 8;
-      ck[i] = (w * CI + i) * (64 / L) + lane / L;
-      const int p = lane % L, col = 16 * ((p >> 1) ^ C::spread(BC, ck[i])) + 8 * (p & 1);
-      cp[i] = cbase + 2 * min(c0 + col, A.cols - 8) + (DW ? 0 : ck[i] * A.ld_c);
+      ck[i] = slab_row<BC>(w * CI + i, lane / L);
+      cp[i] = cbase + 2 * min(c0 + 8 * (lane % L), A.cols - 8) + (DW ? 0 : ck[i] * A.ld_c);
     }
   }
   constexpr int STEP = CF == kAcross ? 64 : 128;  // of `depth`
   const int nst = (depth + STEP - 1) / STEP;
 
-  // dW: rows of the stage after the next one to be fetched
+  // dW: the rows of the next stage to be fetched (past the end the last one, whose address the
+  // zeros then replace; the empty asm keeps the address from being computed under a branch)
   int jr[RI];
   auto rows_of = [&](int s) {
     if constexpr (DW) {
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
-        const int k = s * 64 + rk[i];
-        jr[i] = k < depth ? A.T.row(t.row0 + k) : -1;
+        const int k = t.row0 + min(s * 64 + rk[i], depth - 1);
+        jr[i] = WHOLE ? A.T.perm[k] : k;
       }
     }
   };
+  constexpr int RS = RF == kAcross ? kSlab : 64, CS = CF == kAcross ? kSlab : 64;
   auto issue = [&](typename C::Stage& st, int s) {
     if constexpr (DW) {
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
-        const bool in = jr[i] >= 0;
-        to_lds(in ? rp[i] + jr[i] * A.ld_r : zeros, &st.r[(w * RI + i) * 64]);
-        to_lds(in ? cp[i] + A.share.div(jr[i]) * A.ld_c : zeros, &st.c[(w * CI + i) * 64]);
+        const bool in = s * 64 + rk[i] < depth;
+        const char *r = rp[i] + jr[i] * A.ld_r, *c = cp[i] + A.share.div_any(jr[i]) * A.ld_c;
+        asm("" : "+v"(r), "+v"(c));
+        to_lds(in ? r : zeros, &st.r[(w * RI + i) * RS]);
+        to_lds(in ? c : zeros, &st.c[(w * CI + i) * CS]);
       }
       rows_of(s + 1);
     } else {
@@ -243,10 +254,10 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       const int cleft = CF == kCodes ? left / 4 : left;
 #pragma unroll
       for (int i = 0; i < RI; ++i)
-        to_lds(rk[i] < rleft ? rp[i] + rs : zeros, &st.r[(w * RI + i) * 64]);
+        to_lds(rk[i] < rleft ? rp[i] + rs : zeros, &st.r[(w * RI + i) * RS]);
 #pragma unroll
       for (int i = 0; i < CI; ++i)
-        to_lds(ck[i] < cleft ? cp[i] + cs : zeros, &st.c[(w * CI + i) * 64]);
+        to_lds(ck[i] < cleft ? cp[i] + cs : zeros, &st.c[(w * CI + i) * CS]);
     }
   };
   // scales: this thread's row or column of the tile, 8 bytes a stage (kMxBoth), or one block of
@@ -303,12 +314,11 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(TileArgs A) {
       return base[(tile16 * 16 + l16) * 8 + ((M == kMxW ? kq * 2 + u : u * 4 + kq) ^ ((l16 >> 1) & 7))];
     } else {
       constexpr int B = decltype(width)::value;
-      const int k = u * 32 + kq * 8 + (l16 >> 2);
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + k * B +
-                          16 * (tile16 ^ C::spread(B, k)) + 4 * (l16 & 3);
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + (4 * kq + (l16 >> 2)) * kSlab * 8 +
+                          4 * (l16 & 3) + 16 * tile16 + u * (B == 256 ? 16 * kSlab * 8 : 2 * B);
       typedef __attribute__((address_space(3))) s16x4_t lds4;
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * B));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + B));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       return make_uint4(a.x, a.y, b.x, b.y);
     }
