@@ -21,7 +21,7 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check
-from .sgmv import _check_rows, _stream_handle, _torch, dtype_code
+from .sgmv import _check_rows, _torch, dtype_code
 
 
 def _on(stream):
@@ -29,48 +29,65 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
-def _check_device(*tensors):
-    """Every tensor is on the current GPU (the kernels are launched there)."""
-    here = _torch().cuda.current_device() if tensors[0].is_cuda else -1
+def _stream_of(stream, *tensors) -> int:
+    """The handle of ``stream`` (None: the current one), once every tensor is known to be on the
+    current GPU, where the kernels are launched.  (The raw handle is taken directly: building a
+    Stream object costs as much as the launch.)"""
+    torch = _torch()
+    here = tensors[0].get_device()
     for t in tensors:
-        if t.get_device() != here or here < 0:
-            raise ValueError("tensors must be on the current GPU")
+        if t.get_device() != here:
+            raise ValueError("tensors must be on one GPU")
+    if here < 0 or here != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current GPU")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream.cuda_stream)
 
 
 @dataclasses.dataclass
 class RowGroups:
-    """Group tables on the device (see sgmv_group_rows): rows ``perm[starts[g]:starts[g + 1]]``
-    belong to group g, rows ``perm[starts[n_groups]:]`` to none."""
+    """Group tables on the device (see sgmv_group_rows), int32 [n_groups + 1 + n]: rows
+    ``perm[starts[g]:starts[g + 1]]`` belong to group g, rows ``perm[starts[n_groups]:]`` to
+    none."""
     n: int
     n_groups: int
-    starts: object   # int32 [n_groups + 1]
-    perm: object     # int32 [n]
+    table: object
+
+    @property
+    def starts(self):
+        return self.table[: self.n_groups + 1]
+
+    @property
+    def perm(self):
+        return self.table[self.n_groups + 1:]
 
 
 def group_rows(ids, n_groups: int, stream=None) -> RowGroups:
     """Group tables of a batch whose row i has the id ``ids[i]`` (device int32 [n])."""
-    torch = _torch()
-    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
+    if ids.dtype != _torch().int32 or ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a device int32 tensor [n]")
-    _check_device(ids)
-    n = int(ids.shape[0])
-    with _on(stream):
-        table = torch.empty(n + n_groups + 1, dtype=torch.int32, device=ids.device)
-    starts, perm = table[: n_groups + 1], table[n_groups + 1:]
-    st = _lib.lib().sgmv_group_rows(_stream_handle(stream), ids.data_ptr(), n, n_groups,
-                                    perm.data_ptr(), starts.data_ptr())
+    handle = _stream_of(stream, ids)
+    n = ids.shape[0]
+    if stream is None:
+        table = ids.new_empty(n + n_groups + 1)
+    else:
+        with _on(stream):
+            table = ids.new_empty(n + n_groups + 1)
+    at = table.data_ptr()
+    st = _lib.lib().sgmv_group_rows(handle, ids.data_ptr(), n, n_groups, at + 4 * (n_groups + 1), at)
     check(st, "sgmv_group_rows")
-    return RowGroups(n, n_groups, starts, perm)
+    return RowGroups(n, n_groups, table)
 
 
-def _tables(groups: Optional[RowGroups], n: int):
+def _tables(groups: Optional[RowGroups], n: int, like):
     """(starts, perm, n_groups) for the C calls; None makes all rows one group."""
     if groups is None:
         return None, None, 1
     if groups.n != n:
         raise ValueError(f"{n} rows, but the groups were made of {groups.n}")
-    _check_device(groups.starts, groups.perm)
-    return groups.starts.data_ptr(), groups.perm.data_ptr(), groups.n_groups
+    if groups.table.get_device() != like.get_device():
+        raise ValueError("groups must be on the tensors' GPU")
+    at = groups.table.data_ptr()
+    return at, at + 4 * (groups.n_groups + 1), groups.n_groups
 
 
 def _share(n: int, x_rows: int) -> int:
@@ -111,9 +128,9 @@ def group_matmul(y, x, W, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"x [., {x.shape[1]}] / y [., {y.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt, share = _same_type(y, x, W), _share(n, int(x.shape[0]))
-    starts, perm, E = _tables(groups, n)
-    _check_device(y, x, W)
-    st = _lib.lib().sgmv_group_matmul(_stream_handle(stream), dt, y.data_ptr(), y.stride(0),
+    handle = _stream_of(stream, y, x, W)
+    starts, perm, E = _tables(groups, n, y)
+    st = _lib.lib().sgmv_group_matmul(handle, dt, y.data_ptr(), y.stride(0),
                                       x.data_ptr(), x.stride(0), share, W.data_ptr(), stride,
                                       starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul")
@@ -131,9 +148,9 @@ def group_matmul_dx(dx, dy, W, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"dx [., {dx.shape[1]}] / dy [., {dy.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt = _same_type(dx, dy, W)
-    starts, perm, E = _tables(groups, n)
-    _check_device(dx, dy, W)
-    st = _lib.lib().sgmv_group_matmul_dx(_stream_handle(stream), dt, dx.data_ptr(), dx.stride(0),
+    handle = _stream_of(stream, dx, dy, W)
+    starts, perm, E = _tables(groups, n, dx)
+    st = _lib.lib().sgmv_group_matmul_dx(handle, dt, dx.data_ptr(), dx.stride(0),
                                          dy.data_ptr(), dy.stride(0), W.data_ptr(), stride,
                                          starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul_dx")
@@ -151,9 +168,9 @@ def group_matmul_dw(dW, x, dy, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"x [., {x.shape[1]}] / dy [., {dy.shape[1]}] do not match dW's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt, share = _same_type(dW, x, dy), _share(n, int(x.shape[0]))
-    starts, perm, E = _tables(groups, n)
-    _check_device(dW, x, dy)
-    st = _lib.lib().sgmv_group_matmul_dw(_stream_handle(stream), dt, dW.data_ptr(), stride,
+    handle = _stream_of(stream, dW, x, dy)
+    starts, perm, E = _tables(groups, n, dW)
+    st = _lib.lib().sgmv_group_matmul_dw(handle, dt, dW.data_ptr(), stride,
                                          x.data_ptr(), x.stride(0), share, dy.data_ptr(),
                                          dy.stride(0), starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul_dw")

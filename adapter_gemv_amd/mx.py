@@ -14,8 +14,8 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check
-from .grouped import RowGroups, _check_device, _on, _share, _tables
-from .sgmv import _check_rows, _stream_handle, _torch, dtype_code
+from .grouped import RowGroups, _on, _share, _stream_of, _tables
+from .sgmv import _check_rows, _torch, dtype_code
 
 BLOCK = 32
 
@@ -32,7 +32,8 @@ class MxTensor:
         c, s = self.codes, self.scales
         if c.dtype != uint8 or s.dtype != uint8:
             raise TypeError("codes and scales must be uint8")
-        if c.shape[:-1] != s.shape[:-1] or c.shape[-1] != s.shape[-1] * (BLOCK // 2):
+        cs, ss = tuple(c.shape), tuple(s.shape)
+        if not cs or not ss or cs[:-1] != ss[:-1] or cs[-1] != ss[-1] * (BLOCK // 2):
             raise ValueError(f"codes {tuple(c.shape)} and scales {tuple(s.shape)} do not match: "
                              "[.., h / 2] and [.., h / 32]")
         if not c.is_contiguous() or not s.is_contiguous():
@@ -65,12 +66,13 @@ def mx_quantize(x, stream=None) -> MxTensor:
     if h % BLOCK != 0:
         raise ValueError(f"h = {h} must be a multiple of {BLOCK}")
     dt = dtype_code(x)
-    _check_device(x)
+    handle = _stream_of(stream, x)
+    lead = tuple(x.shape)[:-1]
     with _on(stream):
-        codes = torch.empty((*x.shape[:-1], h // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((*x.shape[:-1], h // BLOCK), dtype=torch.uint8, device=x.device)
-    st = _lib.lib().sgmv_mx_quantize(_stream_handle(stream), dt, codes.data_ptr(),
-                                     scales.data_ptr(), x.data_ptr(), ld, rows, h)
+        codes = x.new_empty((*lead, h // 2), dtype=torch.uint8)
+        scales = x.new_empty((*lead, h // BLOCK), dtype=torch.uint8)
+    st = _lib.lib().sgmv_mx_quantize(handle, dt, codes.data_ptr(), scales.data_ptr(),
+                                     x.data_ptr(), ld, rows, h)
     check(st, "sgmv_mx_quantize")
     return MxTensor(codes, scales)
 
@@ -81,8 +83,8 @@ def mx_dequantize(y, q: MxTensor, stream=None):
         raise ValueError(f"y {tuple(y.shape)} does not match the values' {tuple(q.shape)}")
     rows, h, ld = _as_rows(y, "y")
     dt = dtype_code(y)
-    _check_device(y, q.codes, q.scales)
-    st = _lib.lib().sgmv_mx_dequantize(_stream_handle(stream), dt, y.data_ptr(), ld,
+    handle = _stream_of(stream, y, q.codes, q.scales)
+    st = _lib.lib().sgmv_mx_dequantize(handle, dt, y.data_ptr(), ld,
                                        q.codes.data_ptr(), q.scales.data_ptr(), rows, h)
     check(st, "sgmv_mx_dequantize")
     return y
@@ -92,33 +94,33 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
     """y[i] = x[i // share] @ W[g].T for the rows i of every group g, W [E, h_out, h_in] in MX
     (or [h_out, h_in] with ``groups=None``); rows of no group get zeros.  x is a tensor of
     y's dtype, or an MxTensor: then both sides of the product are in 4 bits."""
-    n = int(y.shape[0])
+    n = y.shape[0]
     _check_rows(y, n, "y")
     E = 1 if groups is None else groups.n_groups
     shape = W.shape if len(W.shape) == 3 else (1, *W.shape)
     if len(shape) != 3 or shape[0] != E:
         raise ValueError(f"W must be [{E}, h_out, h_in]")
-    _, h_out, h_in = (int(v) for v in shape)
-    quantized = isinstance(x, MxTensor)
-    if len(x.shape) != 2 or x.shape[1] != h_in or y.shape[1] != h_out:
-        raise ValueError(f"x {tuple(x.shape)} / y {tuple(y.shape)} do not match W's "
-                         f"h_in = {h_in}, h_out = {h_out}")
-    dt, share = dtype_code(y), _share(n, int(x.shape[0]))
-    starts, perm, n_groups = _tables(groups, n)
-    if quantized:
-        _check_device(y, x.codes, x.scales, W.codes, W.scales)
+    _, h_out, h_in = shape
+    xs = tuple(x.shape)
+    if len(xs) != 2 or xs[1] != h_in or y.shape[1] != h_out:
+        raise ValueError(f"x {xs} / y {tuple(y.shape)} do not match W's h_in = {h_in}, "
+                         f"h_out = {h_out}")
+    dt, share = dtype_code(y), _share(n, xs[0])
+    if isinstance(x, MxTensor):
+        handle = _stream_of(stream, y, x.codes, x.scales, W.codes, W.scales)
+        starts, perm, E = _tables(groups, n, y)
         st = _lib.lib().sgmv_mx_matmul_quantized(
-            _stream_handle(stream), dt, y.data_ptr(), y.stride(0), x.codes.data_ptr(),
-            x.scales.data_ptr(), share, W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n,
-            n_groups, h_in, h_out)
+            handle, dt, y.data_ptr(), y.stride(0), x.codes.data_ptr(), x.scales.data_ptr(), share,
+            W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
         check(st, "sgmv_mx_matmul_quantized")
         return y
-    _check_rows(x, x.shape[0], "x")
+    _check_rows(x, xs[0], "x")
     if x.dtype != y.dtype:
         raise TypeError("x and y must share a dtype")
-    _check_device(y, x, W.codes, W.scales)
+    handle = _stream_of(stream, y, x, W.codes, W.scales)
+    starts, perm, E = _tables(groups, n, y)
     st = _lib.lib().sgmv_mx_matmul(
-        _stream_handle(stream), dt, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0), share,
-        W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, n_groups, h_in, h_out)
+        handle, dt, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0), share, W.codes.data_ptr(),
+        W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_mx_matmul")
     return y

@@ -122,7 +122,7 @@ def test_binding_refusals():
     x, y = torch.zeros(6, 64, dtype=bf), torch.zeros(12, 32, dtype=bf)
     Wt = torch.zeros(3, 32, 64, dtype=bf)
     i32 = torch.int32
-    g = grouped.RowGroups(12, 3, torch.zeros(4, dtype=i32), torch.zeros(12, dtype=i32))
+    g = grouped.RowGroups(12, 3, torch.zeros(16, dtype=i32))
     for bad in (lambda: grouped.group_matmul(y[:11], x, Wt, g),                  # 11 rows share 6
                 lambda: grouped.group_matmul(y, x, Wt[:2], g),                   # two groups' weights
                 lambda: grouped.group_matmul(y, x[:, :56], Wt, g),               # h_in
