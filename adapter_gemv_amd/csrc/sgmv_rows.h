@@ -42,61 +42,57 @@ __device__ inline int wave_scan(int v) {
   return v;
 }
 
-// How many tiles of at most BM rows the groups make (the rows of no group are tiled too,
-// behind them, if `rest`): wave-uniform, every lane of the wave takes part.
-__device__ inline int lane_tiles(const RowTab& T, int g, int BM, bool rest, int* first, int* len) {
-  const int last = rest ? T.G : T.G - 1;
-  int a = 0, b = 0;
-  if (g <= last) {
-    a = T.starts[g];
-    b = g < T.G ? T.starts[g + 1] : T.n;
-  }
-  *first = a;
-  *len = b - a;
-  return (b - a + BM - 1) / BM;
-}
-
-// The tiles of all groups, counted and found by one wavefront: 64 groups at a time, one to a
-// lane.  `count` is their number; find(m) is the m-th (0 <= m < count).  Both are uniform.
+// The row tiles of all groups, at most BM rows each, counted and found by one wavefront: 64
+// groups at a time, one to a lane.  A group's tiles stand together, the rows of no group behind
+// them all.  Everything returned is uniform.
 struct TileList {
   RowTab T;
   int BM;
-  bool rest;
   int count;
   int first, len, incl;  // this lane's group of the first 64, and its inclusive tile count
 
-  __device__ TileList(const RowTab& t, int bm, bool with_rest) : T(t), BM(bm), rest(with_rest) {
+  // tiles of group g (G: the rows of none)
+  __device__ int tiles(int g, int* f, int* l) const {
+    int a = 0, b = 0;
+    if (g <= T.G) {
+      a = T.starts[g];
+      b = g < T.G ? T.starts[g + 1] : T.n;
+    }
+    *f = a;
+    *l = b - a;
+    return (b - a + BM - 1) / BM;
+  }
+
+  __device__ TileList(const RowTab& t, int bm) : T(t), BM(bm) {
     if (!T.starts) {
       count = (T.n + BM - 1) / BM;
       return;
     }
     const int lane = threadIdx.x & 63;
-    incl = wave_scan(lane_tiles(T, lane, BM, rest, &first, &len));
+    incl = wave_scan(tiles(lane, &first, &len));
     count = __builtin_amdgcn_readlane(incl, 63);
     for (int g0 = 64; g0 <= T.G; g0 += 64) {
       int f, l;
-      count += __builtin_amdgcn_readlane(wave_scan(lane_tiles(T, g0 + lane, BM, rest, &f, &l)), 63);
+      count += __builtin_amdgcn_readlane(wave_scan(tiles(g0 + lane, &f, &l)), 63);
     }
   }
 
   __device__ RowTile find(int m) const {
     if (!T.starts) return {0, m * BM, min(BM, T.n - m * BM)};
     const int lane = threadIdx.x & 63;
-    int f = first, l = len, in = incl, before = 0, g0 = 0;
-    for (;;) {
+    int f = first, l = len, in = incl, before = 0;
+    for (int g0 = 0; g0 <= T.G; g0 += 64) {
+      if (g0) in = wave_scan(tiles(g0 + lane, &f, &l));
       const uint64_t past = __ballot(before + in > m);
       if (past) {
         const int who = __builtin_ctzll(past);
         const int gf = __builtin_amdgcn_readlane(f, who), gl = __builtin_amdgcn_readlane(l, who);
-        const int tiles = (gl + BM - 1) / BM;
-        const int at = m - (before + __builtin_amdgcn_readlane(in, who) - tiles);
+        const int at = m - (before + __builtin_amdgcn_readlane(in, who) - (gl + BM - 1) / BM);
         return {g0 + who, gf + at * BM, min(BM, gl - at * BM)};
       }
       before += __builtin_amdgcn_readlane(in, 63);
-      g0 += 64;
-      if (g0 > T.G) return {T.G, 0, 0};
-      in = wave_scan(lane_tiles(T, g0 + lane, BM, rest, &f, &l));
     }
+    return {T.G, 0, 0};
   }
 };
 
@@ -129,8 +125,8 @@ inline int32_t shared_rows(int32_t n, int32_t share) { return (n + share - 1) / 
 
 // at most this many row tiles of BM rows in the groups and behind them
 inline int64_t max_row_tiles(int32_t n, int32_t G, bool grouped, int BM) {
-  const int64_t full = n / BM + (grouped ? G + 1 : 1);
-  return full < n ? full : n;
+  const int64_t most = n / BM + (grouped ? G + 1 : 1);
+  return most < n ? most : n;
 }
 
 // whether the tiles of a product of n rows and `cols` columns can be launched, at the smallest

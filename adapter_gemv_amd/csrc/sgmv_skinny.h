@@ -227,7 +227,7 @@ template <int DT, bool MX, int CT>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(SkinnyArgs A) {
   __shared__ __attribute__((aligned(16))) float sums[kSkinnyWaves][16][16 * CT + 4];
   const int ct = (A.h_out + 16 * CT - 1) / (16 * CT);
-  const TileList list(A.T, kSkinnyRows, true);
+  const TileList list(A.T, kSkinnyRows);
   const int m = blockIdx.x / ct, c0 = (blockIdx.x - m * ct) * 16 * CT;
   if (m >= list.count) return;
   const RowTile t = list.find(m);
