@@ -35,11 +35,20 @@ __global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restr
   const int run = ((n + waves - 1) / waves + 63) & ~63;
   const int lo = min(n, w * run), hi = min(n, lo + run);
   int* mine = bins + w * B;
-  auto bin_of = [&](int i) {
-    const int id = i < hi ? ids[i] : 0;
-    return static_cast<uint32_t>(id) < static_cast<uint32_t>(G) ? id : G;
+  auto bin_of = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(G) ? id : G; };
+  // ids come eight at a time: one trip to memory for 512 rows of the wavefront
+  constexpr int U = 8;
+  int id[U];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = ids[min(i0 + 64 * u + lane, hi - 1)];
   };
-  for (int i = lo + lane; i < hi; i += 64) atomicAdd(&mine[bin_of(i)], 1);
+  for (int i0 = lo; i0 < hi; i0 += 64 * U) {
+    fetch(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + 64 * u + lane < hi) atomicAdd(&mine[bin_of(id[u])], 1);
+  }
   __syncthreads();
   // exclusive sums over bins, then over a bin's wavefronts
   int carry = 0;
@@ -66,24 +75,28 @@ __global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restr
   }
   const int bits = 32 - __builtin_clz(static_cast<uint32_t>(G));
   volatile int* next = mine;
-  for (int i0 = lo; i0 < hi; i0 += 64) {
-    const int i = i0 + lane;
-    const bool in = i < hi;
-    const int b = bin_of(i);
-    uint64_t same = __ballot(in);
-    for (int k = 0; k < bits; ++k) {
-      const uint64_t set = __ballot((b >> k) & 1);
-      same &= (b >> k) & 1 ? set : ~set;
+  for (int i0 = lo; i0 < hi; i0 += 64 * U) {
+    fetch(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 64 * u + lane;
+      const bool in = i < hi;
+      const int b = bin_of(id[u]);
+      uint64_t same = __ballot(in);
+      for (int k = 0; k < bits; ++k) {
+        const uint64_t set = __ballot((b >> k) & 1);
+        same &= (b >> k) & 1 ? set : ~set;
+      }
+      if (in) {
+        const int below = __popcll(same & ((uint64_t(1) << lane) - 1));
+        const int base = next[b];
+        perm[base + below] = i;
+        // the bin's last lane moves its next free place on, after every lane read it (LDS
+        // accesses of one wavefront keep their order)
+        if ((same >> lane) == 1) next[b] = base + below + 1;
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-    if (in) {
-      const int below = __popcll(same & ((uint64_t(1) << lane) - 1));
-      const int base = next[b];
-      perm[base + below] = i;
-      // the bin's last lane moves its next free place on, after every lane read it (LDS
-      // accesses of one wavefront keep their order)
-      if ((same >> lane) == 1) next[b] = base + below + 1;
-    }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -105,7 +118,10 @@ hipError_t launch_dw(hipStream_t s, const TileArgs& A) {
 
 hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
   const bool f16 = dtype == SGMV_F16;
-  if (A.T.n / A.T.G >= TILE_BIG)
+  const auto tiles = [&](int B) {
+    return static_cast<double>(A.T.G) * ((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
+  };
+  if (big_tiles(tiles(256), tiles(128)))
     return f16 ? launch_dw<SGMV_F16, 256, 2, 4>(s, A) : launch_dw<SGMV_BF16, 256, 2, 4>(s, A);
   return f16 ? launch_dw<SGMV_F16, 128, 2, 2>(s, A) : launch_dw<SGMV_BF16, 128, 2, 2>(s, A);
 }

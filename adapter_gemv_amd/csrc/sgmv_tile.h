@@ -40,6 +40,8 @@
 // columns past the end repeat the last one and are not stored.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "sgmv_skinny.h"
@@ -419,19 +421,22 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
 
   // lane (l16, kq): row l16 of a fragment, columns 8 * (kq >> 1) .. + 7 of column tile
   // j + (kq & 1) after the exchange
+  int row[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int q = (wr * NR + i) * 16 + l16;
-    bool in;
-    int64_t row;
-    if constexpr (DW) {
-      in = r0 + q < A.rows;
-      row = r0 + q;
-    } else {
-      in = q < t.rows;
-      row = in ? A.T.row(t.row0 + q) : 0;
-    }
-    uint16_t* to = A.out + (DW ? static_cast<int64_t>(t.g) * A.out_group : 0) + row * A.ld_out;
+    row[i] = DW ? r0 + q : t.row0 + min(q, t.rows - 1);
+  }
+  if (!DW && A.T.perm) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) row[i] = A.T.perm[row[i]];
+  }
+  uint16_t* const out = A.out + (DW ? static_cast<int64_t>(t.g) * A.out_group : 0);
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int q = (wr * NR + i) * 16 + l16;
+    const bool in = DW ? row[i] < A.rows : q < t.rows;
+    uint16_t* to = out + row[i] * A.ld_out;
 #pragma unroll
     for (int j = 0; j < NC; j += 2) {
       using E = Elem<DT>;
@@ -445,8 +450,19 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   }
 }
 
-#ifndef TILE_BIG
-#define TILE_BIG 192
+// Tile size.  256 x 256 (one workgroup to a CU) runs full tiles at 1.2 times the rate of
+// 128 x 128 (two to a CU; 8192^3, bfloat16: 1370 and 1154 TFLOP/s), but wastes more where groups
+// or columns end and needs four times the tiles' room to fill the card.  What counts is rounds of
+// the 256 CUs: a round of 128 x 128 tiles takes 0.65 to 0.73 of one of 256 x 256 (measured at
+// 8 groups of 256 to 1024 rows).  A group's last tile is taken to be half full.
+constexpr int kCus = 256;
+
+#ifdef TILE_BIG
+inline bool big_tiles(double, double) { return TILE_BIG == 0; }
+#else
+inline bool big_tiles(double tiles256, double tiles128) {
+  return std::ceil(tiles256 / kCus) <= 0.68 * std::ceil(tiles128 / (2 * kCus));
+}
 #endif
 
 template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
@@ -459,17 +475,19 @@ hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
 // row tiles of every group (and of the rows of none) times column tiles
 template <Mode M, bool WHOLE = true>
 hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
-  const int avg = A.T.n / A.T.G;
-  const auto tiles = [&](int BR, int BC) {
-    return sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, BR) * ((A.cols + BC - 1) / BC);
+  const auto columns = [&](int BC) { return (A.cols + BC - 1) / BC; };
+  const auto expected = [&](int B) {
+    return (static_cast<double>(A.T.n) / B + 0.5 * std::min(A.T.n, A.T.G)) * columns(B);
   };
   const bool f16 = dtype == SGMV_F16;
-  if (avg >= TILE_BIG) {
-    return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, tiles(256, 256), A)
-               : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, tiles(256, 256), A);
+  if (big_tiles(expected(256), expected(128))) {
+    const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 256) * columns(256);
+    return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A)
+               : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A);
   }
-  return f16 ? launch_tile<SGMV_F16, M, 128, 128, 2, 2, WHOLE>(s, tiles(128, 128), A)
-             : launch_tile<SGMV_BF16, M, 128, 128, 2, 2, WHOLE>(s, tiles(128, 128), A);
+  const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 128) * columns(128);
+  return f16 ? launch_tile<SGMV_F16, M, 128, 128, 2, 2, WHOLE>(s, tiles, A)
+             : launch_tile<SGMV_BF16, M, 128, 128, 2, 2, WHOLE>(s, tiles, A);
 }
 
 }  // namespace sgmv_dev
