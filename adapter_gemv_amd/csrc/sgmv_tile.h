@@ -3,8 +3,8 @@
 // One workgroup makes a BR x BC tile of the output with MFMA 16x16 tiles: BR output rows (rows
 // of a group, or rows of dW) by BC output columns.  Both operands come in stages of 128 bytes
 // along the contracted dimension (64 16-bit elements, or 256 4-bit ones) by direct
-// global-to-LDS loads into one of two stage buffers while the other is multiplied, so a stage
-// costs one barrier and its loads have the whole previous stage to arrive.
+// global-to-LDS loads into one of two or three stage buffers while another is multiplied, so a
+// stage costs one barrier and its loads have at least most of the previous stage to arrive.
 //
 // An operand lies either along its rows (kAlong: each tile row's stage is 128 contiguous
 // bytes, a fragment is one 16-byte LDS read per lane) or across them (kAcross: the contracted
@@ -59,14 +59,16 @@ typedef __attribute__((address_space(1))) void tile_global_void;
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 // 16 bytes per lane from src into LDS at dst + 16 * lane (dst the same for the wavefront)
-__device__ inline void to_lds(const char* src, uint4* dst) {
+__device__ inline void to_lds(const char* src, u32x4_t* dst) {
   __builtin_amdgcn_global_load_lds((tile_global_void*)src, (tile_lds_void*)dst, 16, 0, 0);
 }
 
-// every global load of this wavefront has landed, and every LDS access of it is done
+// at most N (< 16) global loads of this wavefront are in flight, and every LDS access of it is
+// done; then the workgroup's barrier
+template <int N>
 __device__ inline void wait_stage() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt 0, lgkmcnt 0
+  __builtin_amdgcn_s_waitcnt(N | (7 << 4));  // vmcnt N, lgkmcnt 0
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
@@ -124,11 +126,15 @@ struct Tile {
   struct MxScales {
     uint8_t b[M == kMxBoth ? 8 * (BR + BC) : M == kMxW ? 2 * BC : 16];
   };
-  struct Stage {
-    uint4 r[RF == kAcross ? BR / 8 * kSlab : BR * 8];
-    uint4 c[CF == kAcross ? BC / 8 * kSlab : BC * CP];
-    MxScales s;
+  // LDS buffers.  kForward's 256 x 256 tile has room for a third one of the column operand: the
+  // weight comes from HBM, the rows from the L2, so it is fetched two stages ahead.
+  struct RBuf {
+    u32x4_t v[RF == kAcross ? BR / 8 * kSlab : BR * 8];
   };
+  struct CBuf {
+    u32x4_t v[CF == kAcross ? BC / 8 * kSlab : BC * CP];
+  };
+  static constexpr int DC = M == kForward && BR == 256 ? 3 : 2;
 };
 
 constexpr int kTileXcds = 8;
@@ -150,7 +156,10 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI;
   constexpr Form RF = C::RF, CF = C::CF;
   constexpr bool DW = C::DW;
-  __shared__ typename C::Stage b0, b1;
+  __shared__ typename C::RBuf rb0, rb1;
+  __shared__ typename C::CBuf cb0, cb1;
+  __shared__ typename C::MxScales sb0, sb1;
+  constexpr int DC = C::DC;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
   const int wr = w / WC, wc = w % WC;
 
@@ -237,30 +246,37 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
     }
   };
   constexpr int RS = RF == kAcross ? kSlab : 64, CS = CF == kAcross ? kSlab : 64;
-  auto issue = [&](typename C::Stage& st, int s) {
-    if constexpr (DW) {
-#pragma unroll
-      for (int i = 0; i < RI; ++i) {
-        const bool in = s * 64 + rk[i] < depth;
-        const char *r = rp[i] + jr[i] * A.ld_r, *c = cp[i] + A.share.div_any(jr[i]) * A.ld_c;
-        asm("" : "+v"(r), "+v"(c));
-        to_lds(in ? r : zeros, &st.r[(w * RI + i) * RS]);
-        to_lds(in ? c : zeros, &st.c[(w * CI + i) * CS]);
-      }
-      rows_of(s + 1);
-    } else {
-      const int64_t rs = static_cast<int64_t>(s) * 128;
-      const int64_t cs = CF == kAlong ? rs : CF == kCodes ? rs / 4 : s * 64 * A.ld_c;
-      const int left = depth - s * STEP;
-      const int rleft = CF == kAcross ? 2 * left : left;  // r lies along its rows: bytes
-      const int cleft = CF == kCodes ? left / 4 : left;
-#pragma unroll
-      for (int i = 0; i < RI; ++i)
-        to_lds(rk[i] < rleft ? rp[i] + rs : zeros, &st.r[(w * RI + i) * RS]);
-#pragma unroll
-      for (int i = 0; i < CI; ++i)
-        to_lds(ck[i] < cleft ? cp[i] + cs : zeros, &st.c[(w * CI + i) * CS]);
-    }
+  // the k-th load of stage s (kDw: the k-th of each operand), of LOADS
+  constexpr int LOADS = DW ? RI : RI + CI;
+  auto issue_r = [&](typename C::RBuf& to, int s, auto which) __attribute__((always_inline)) {
+    constexpr int i = decltype(which)::value;
+    const int left = (depth - s * STEP) * (CF == kAcross ? 2 : 1);  // r lies along its rows: bytes
+    to_lds(rk[i] < left ? rp[i] + static_cast<int64_t>(s) * 128 : zeros, &to.v[(w * RI + i) * RS]);
+  };
+  auto issue_c = [&](typename C::CBuf& to, int s, auto which) __attribute__((always_inline)) {
+    constexpr int i = decltype(which)::value;
+    const int64_t cs = CF == kAlong ? s * int64_t{128} : CF == kCodes ? s * int64_t{32} : s * 64 * A.ld_c;
+    const int left = (depth - s * STEP) / (CF == kCodes ? 4 : 1);
+    const char* c = cp[i] + cs;
+    if constexpr (CF == kAcross) asm("" : "+v"(c));  // keeps its computation out of a branch
+    to_lds(ck[i] < left ? c : zeros, &to.v[(w * CI + i) * CS]);
+  };
+  auto issue_dw = [&](typename C::RBuf& rt, typename C::CBuf& ct, int s, auto which) __attribute__((always_inline)) {
+    constexpr int k = decltype(which)::value;
+    const bool in = s * 64 + rk[k] < depth;
+    const char *r = rp[k] + jr[k] * A.ld_r, *c = cp[k] + A.share.div_any(jr[k]) * A.ld_c;
+    asm("" : "+v"(r), "+v"(c));
+    to_lds(in ? r : zeros, &rt.v[(w * RI + k) * RS]);
+    to_lds(in ? c : zeros, &ct.v[(w * CI + k) * CS]);
+    if constexpr (k == LOADS - 1) rows_of(s + 1);
+  };
+  // one of the loads behind stage s: of the rows of the next one, or of the columns of the last
+  // one that fits
+  auto issue_one = [&](typename C::RBuf& rt, typename C::CBuf& ct, int s, auto which) __attribute__((always_inline)) {
+    constexpr int k = decltype(which)::value;
+    if constexpr (DW) issue_dw(rt, ct, s + 1, which);
+    else if constexpr (k < RI) issue_r(rt, s + 1, which);
+    else issue_c(ct, s + DC - 1, std::integral_constant<int, k - RI>{});
   };
   // scales: this thread's row or column of the tile, 8 bytes a stage (kMxBoth), or one block of
   // a column, 1 byte (kMxW); fetched a stage ahead and put into LDS behind the products
@@ -301,56 +317,79 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
       sv[0] = k < blocks ? b : 127u;
     }
   };
-  auto store_scales = [&](typename C::Stage& st) {  // no branch: see the loop below
+  auto store_scales = [&](typename C::MxScales& to) {  // no branch: see the loop below
     if constexpr (M == kMxBoth) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint16_t*>(st.s.b + sto + k * (WR * NR * 32)) =
+        *reinterpret_cast<uint16_t*>(to.b + sto + k * (WR * NR * 32)) =
             static_cast<uint16_t>(__builtin_amdgcn_perm(sv[1], sv[0], k | (4 + k) << 8));
     } else if constexpr (M == kMxW) {
-      st.s.b[sto] = static_cast<uint8_t>(sv[0]);
+      to.b[sto] = static_cast<uint8_t>(sv[0]);
     }
   };
-  auto fragment = [&](auto form, auto width, const uint4* base, int tile16, int u) -> uint4 {
+  // Fragment reads.  Each address is one lane offset, made here, plus a constant: the compiler
+  // tells LDS buffers apart (and so does not wait for loads into another one) only where the
+  // address is a few steps from the buffer's name.
+  auto lane_at = [&](auto form, int tile, int u) __attribute__((always_inline)) {
+    constexpr Form F = decltype(form)::value;
+    if constexpr (F == kAlong)  // 16-byte pieces
+      return (tile * 16 + l16) * 8 + ((M == kMxW ? kq * 2 + u : u * 4 + kq) ^ ((l16 >> 1) & 7));
+    else if constexpr (F == kCodes)  // 8-byte pieces
+      return (tile * 16 + l16) * 4 + kq;
+    else  // 8-byte pieces
+      return (4 * kq + (l16 >> 2)) * kSlab * 2 + (l16 & 3) + 4 * tile;
+  };
+  using FormR = std::integral_constant<Form, RF>;
+  using FormC = std::integral_constant<Form, CF>;
+  int ro[2] = {lane_at(FormR{}, wr * NR, 0), lane_at(FormR{}, wr * NR, 1)};
+  int co[2] = {lane_at(FormC{}, wc * NC, 0), lane_at(FormC{}, wc * NC, 1)};
+  asm("" : "+v"(ro[0]), "+v"(ro[1]), "+v"(co[0]), "+v"(co[1]));
+  auto fragment = [&](auto form, auto width, const u32x4_t* base, const int* at, int i,
+                      int u) __attribute__((always_inline)) -> uint4 {
     if constexpr (decltype(form)::value == kAlong) {
-      return base[(tile16 * 16 + l16) * 8 + ((M == kMxW ? kq * 2 + u : u * 4 + kq) ^ ((l16 >> 1) & 7))];
+      const u32x4_t v = base[at[u] + i * 128];
+      return make_uint4(v.x, v.y, v.z, v.w);
     } else {
       constexpr int B = decltype(width)::value;
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + (4 * kq + (l16 >> 2)) * kSlab * 8 +
-                          4 * (l16 & 3) + 16 * tile16 + u * (B == 256 ? 16 * kSlab * 8 : 2 * B);
       typedef __attribute__((address_space(3))) s16x4_t lds4;
+      const u32x2_t* p = reinterpret_cast<const u32x2_t*>(base) + at[0] + 4 * i +
+                         u * (B == 256 ? 16 * kSlab * 2 : B / 2);
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + B));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + B / 4));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       return make_uint4(a.x, a.y, b.x, b.y);
     }
   };
-  auto rfrag = [&](const typename C::Stage& st, int i, int u) {
-    return fragment(std::integral_constant<Form, RF>{}, std::integral_constant<int, BR>{}, st.r,
-                    wr * NR + i, u);
+  auto rfrag = [&](const typename C::RBuf& from, int i, int u) __attribute__((always_inline)) {
+    return fragment(FormR{}, std::integral_constant<int, BR>{}, from.v, ro, i, u);
   };
-  auto cfrag = [&](const typename C::Stage& st, int j, int u) {
-    return fragment(std::integral_constant<Form, CF>{}, std::integral_constant<int, BC>{}, st.c,
-                    wc * NC + j, u);
+  auto cfrag = [&](const typename C::CBuf& from, int j, int u) __attribute__((always_inline)) {
+    return fragment(FormC{}, std::integral_constant<int, BC>{}, from.v, co, j, u);
   };
   // One stage: row fragments in runs of NQ, each 2 * NQ steps (both halves of the stage) of NC
   // MFMAs on one row fragment.  The next step's row fragment is read during a step, the second
-  // half's column fragments during the first run's last steps of the first half; the fences
-  // keep the compiler from hoisting more reads than there are registers for.  Short runs halve
-  // the time between two uses of an accumulator's neighbours' operands and measured faster
-  // (8192^3, bfloat16: forward 1337 -> 1358, 4-bit weights 1047 -> 1273 TFLOP/s), except for dx
-  // (1329 -> 1246: the compiler then waits for the loads in flight in mid-stage).
-  constexpr int NQ = M == kDx ? NR : NR / 4;
+  // half's column fragments during the first run's steps of the first half, and each of the
+  // first steps issues one of the loads behind the stage: all at once, at the stage's start,
+  // they hold up every wavefront for as long as the CU takes to accept 64 KB (8192^3, bfloat16:
+  // forward 1370, dx 1350, dW 1270 TFLOP/s that way; 1470, 1400, 1300 spread out).  With two
+  // workgroups to a CU the other one has work meanwhile, and what counts is that the loads
+  // arrive in a stage of half the length (8 groups of 1024 rows, 4096 x 4096, 128 x 128 tiles:
+  // 913 TFLOP/s at once, 871 spread out).  The fences keep the compiler from hoisting more reads
+  // than there are registers for.
+  constexpr int NQ = NR / 4;
+  constexpr bool SPREAD = BR == 256;
   constexpr int PER = NC > NQ ? NC / NQ : 1, FROM = NQ - NC / PER;  // column fragments of a step
-  auto stage = [&](const typename C::Stage& st, typename C::Stage& next, int s) __attribute__((always_inline)) {
+  auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb, const typename C::MxScales& sb,
+                   typename C::RBuf& rn, typename C::CBuf& cn, typename C::MxScales& sn,
+                   int s) __attribute__((always_inline)) {
     uint4 cv[2][NC], rv[2];
     uint32_t rs[NR / 2], cs[NC / 2];
     if constexpr (M == kMxW) {
-      uint2 codes[NC];
-      const uint8_t* from = st.s.b + (((kq >> 1) * WC + wc) * 16 + l16) * NC;
+      u32x2_t codes[NC];
+      const uint8_t* from = sb.b + (((kq >> 1) * WC + wc) * 16 + l16) * NC;
 #pragma unroll
       for (int j = 0; j < NC; ++j)
-        codes[j] = reinterpret_cast<const uint2*>(st.c)[((wc * NC + j) * 16 + l16) * 4 + kq];
+        codes[j] = reinterpret_cast<const u32x2_t*>(cb.v)[co[0] + 64 * j];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const float f = mx_scale(from[j]);
@@ -359,27 +398,28 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < NC; ++j) cv[0][j] = cfrag(st, j, 0);
+      for (int j = 0; j < NC; ++j) cv[0][j] = cfrag(cb, j, 0);
     }
     if constexpr (M == kMxBoth) {
-      const uint32_t* r = reinterpret_cast<const uint32_t*>(st.s.b + ((kq * WR + wr) * 16 + l16) * NR * 2);
-      const uint32_t* c = reinterpret_cast<const uint32_t*>(st.s.b + C::SC + ((kq * WC + wc) * 16 + l16) * NC * 2);
+      const uint32_t* r = reinterpret_cast<const uint32_t*>(sb.b + ((kq * WR + wr) * 16 + l16) * NR * 2);
+      const uint32_t* c = reinterpret_cast<const uint32_t*>(sb.b + C::SC + ((kq * WC + wc) * 16 + l16) * NC * 2);
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) rs[i] = r[i];
 #pragma unroll
       for (int j = 0; j < NC / 2; ++j) cs[j] = c[j];
     }
-    rv[0] = rfrag(st, 0, 0);
+    rv[0] = rfrag(rb, 0, 0);
     fetch_scales(s + 1);
-    issue(next, s + 1);
+    if constexpr (!SPREAD) tile_for<0, LOADS>([&](auto k) __attribute__((always_inline)) { issue_one(rn, cn, s, k); });
     __builtin_amdgcn_sched_barrier(0);
     tile_for<0, 2 * NR>([&](auto step) __attribute__((always_inline)) {
       constexpr int n = decltype(step)::value, u = n / NQ % 2, i = n / (2 * NQ) * NQ + n % NQ;
       constexpr int n1 = n + 1, u1 = n1 / NQ % 2, i1 = n1 / (2 * NQ) * NQ + n1 % NQ;
-      if constexpr (n1 < 2 * NR) rv[n1 & 1] = rfrag(st, i1, u1);
+      if constexpr (n1 < 2 * NR) rv[n1 & 1] = rfrag(rb, i1, u1);
+      if constexpr (SPREAD && n < LOADS) issue_one(rn, cn, s, step);
       if constexpr (M != kMxW && n < NQ && n >= FROM) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) cv[1][(n - FROM) * PER + j] = cfrag(st, (n - FROM) * PER + j, 1);
+        for (int j = 0; j < PER; ++j) cv[1][(n - FROM) * PER + j] = cfrag(cb, (n - FROM) * PER + j, 1);
       }
       uint4 hi, lo;
       if constexpr (M == kMxW && DT == SGMV_F16) f16_split(rv[n & 1], &hi, &lo);
@@ -400,23 +440,47 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
       });
       __builtin_amdgcn_sched_barrier(0);
     });
-    store_scales(next);
+    store_scales(sn);
   };
 
-  // stages in pairs, one to a buffer (an odd count's last stage, and the one fetched behind the
-  // end, are zeros): no branch inside the loop, which keeps the accumulators where they are
+  // No branch inside the loop, which keeps the accumulators where they are: stages go in pairs
+  // (an odd count's last one is zeros), or in sixes where the columns have three buffers, with
+  // the remainder behind the loop; what is fetched behind the end is zeros.
   if (nst > 0) {
     rows_of(0);
     fetch_scales(0);
-    issue(b0, 0);
-    store_scales(b0);
-    for (int s = 0; s < nst; s += 2) {
-      wait_stage();
-      stage(b0, b1, s);
-      wait_stage();
-      stage(b1, b0, s + 1);
+    if constexpr (DW) {
+      tile_for<0, RI>([&](auto k) __attribute__((always_inline)) { issue_dw(rb0, cb0, 0, k); });
+    } else {
+      tile_for<0, RI>([&](auto k) __attribute__((always_inline)) { issue_r(rb0, 0, k); });
+      tile_for<0, CI>([&](auto k) __attribute__((always_inline)) { issue_c(cb0, 0, k); });
     }
-    wait_stage();  // the last loads into LDS land before the workgroup can end
+    store_scales(sb0);
+    if constexpr (DC == 2) {
+      for (int s = 0; s < nst; s += 2) {
+        wait_stage<0>();
+        stage(rb0, cb0, sb0, rb1, cb1, sb1, s);
+        wait_stage<0>();
+        stage(rb1, cb1, sb1, rb0, cb0, sb0, s + 1);
+      }
+    } else {
+      __shared__ typename C::CBuf cb2;
+      tile_for<0, CI>([&](auto k) __attribute__((always_inline)) { issue_c(cb1, 1, k); });
+      auto nth = [&](auto which, int s) __attribute__((always_inline)) {
+        constexpr int k = decltype(which)::value;
+        typename C::RBuf &r = k % 2 ? rb1 : rb0, &rn = k % 2 ? rb0 : rb1;
+        typename C::CBuf &c = k % 3 == 0 ? cb0 : k % 3 == 1 ? cb1 : cb2;
+        typename C::CBuf &cn = k % 3 == 0 ? cb2 : k % 3 == 1 ? cb0 : cb1;
+        wait_stage<CI>();
+        stage(r, c, sb0, rn, cn, sb0, s + k);
+      };
+      int s = 0;
+      for (; s + 6 <= nst; s += 6) tile_for<0, 6>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
+      tile_for<0, 5>([&](auto k) __attribute__((always_inline)) {
+        if (s + decltype(k)::value < nst) nth(k, s);
+      });
+    }
+    wait_stage<0>();  // the last loads into LDS land before the workgroup can end
   }
 
   // lane (l16, kq): row l16 of a fragment, columns 8 * (kq >> 1) .. + 7 of column tile
@@ -450,10 +514,10 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   }
 }
 
-// Tile size.  256 x 256 (one workgroup to a CU) runs full tiles at 1.2 times the rate of
-// 128 x 128 (two to a CU; 8192^3, bfloat16: 1370 and 1154 TFLOP/s), but wastes more where groups
+// Tile size.  256 x 256 (one workgroup to a CU) runs full tiles at 1.3 times the rate of
+// 128 x 128 (two to a CU; 8192^3, bfloat16: 1470 and 1150 TFLOP/s), but wastes more where groups
 // or columns end and needs four times the tiles' room to fill the card.  What counts is rounds of
-// the 256 CUs: a round of 128 x 128 tiles takes 0.65 to 0.73 of one of 256 x 256 (measured at
+// the 256 CUs: a round of 128 x 128 tiles takes 0.64 to 0.75 of one of 256 x 256 (measured at
 // 8 groups of 256 to 1024 rows).  A group's last tile is taken to be half full.
 constexpr int kCus = 256;
 
@@ -461,7 +525,7 @@ constexpr int kCus = 256;
 inline bool big_tiles(double, double) { return TILE_BIG == 0; }
 #else
 inline bool big_tiles(double tiles256, double tiles128) {
-  return std::ceil(tiles256 / kCus) <= 0.68 * std::ceil(tiles128 / (2 * kCus));
+  return std::ceil(tiles256 / kCus) <= 0.7 * std::ceil(tiles128 / (2 * kCus));
 }
 #endif
 
