@@ -14,60 +14,113 @@ constexpr int kMxBlock = 32;
 // rows per group, on average, below which the streaming kernel runs
 constexpr int kMxSkinnyMost = 48;
 
-// Four lanes to a block of 32, 8 elements (16 bytes) each: a wavefront reads 1 KB and writes
-// 256 bytes of codes in one access each.  The block's largest magnitude is the largest of the
-// magnitudes' bit patterns (a NaN's pattern is above infinity's, so neither is lost).
+// Both kernels move every byte once and are bound by that: four lanes to a block of 32, 8
+// elements (16 bytes of values, 4 of codes) each, so a wavefront's accesses are whole lines, and
+// kMxPer pieces a thread, all loads first.  Rows without gaps are one long row (no division).
+constexpr int kMxPer = 4;
+
+struct MxSpan {
+  int64_t pieces, per_row, ld;  // pieces of 8 elements; elements between rows
+  // the first element of piece i of a strided matrix
+  __device__ int64_t at(int64_t i) const {
+    if (per_row == 0) return 8 * i;
+    const int64_t row = i / per_row;
+    return row * ld + 8 * (i - row * per_row);
+  }
+};
+
+// The scale byte of a block whose largest magnitude has the bits `top` (the magnitudes' patterns
+// order like the magnitudes, with infinity and NaN above them all): the exponent of
+// 2^(floor(log2) - 2) with bias 127, at least 0.
 template <int DT>
-__global__ __launch_bounds__(256) void mx_quantize_kernel(uint32_t* __restrict__ codes,
-                                                          uint8_t* __restrict__ scales,
-                                                          const uint16_t* __restrict__ x, int64_t ld,
-                                                          int64_t rows, int32_t h) {
-  const int64_t per_row = h / 8, total = rows * per_row;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= total) return;  // h / 8 is a multiple of 4: a block's lanes leave together
-  const int64_t row = i / per_row, at = i % per_row;
-  const uint4 v = ld16(x + row * ld + 8 * at);
-  float f[8];
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    f[e] = elem<DT>(v, e);
-    top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+__device__ inline uint32_t mx_scale_byte(uint32_t top) {
+  if constexpr (DT == SGMV_BF16) {
+    const int e = static_cast<int>(top >> 7);  // subnormals: below 2^-126, so 0 as well
+    return static_cast<uint32_t>(max(e - 2, 0));
+  } else {
+    const uint32_t e = top >> 10;
+    if (e) return e + 110;
+    return top ? 101 + 31 - __builtin_clz(top) : 0;
   }
-  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 1)));
-  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 2)));
-  const bool finite = top < 0x7f800000u;
-  const int e = top == 0 ? -127 : max(__builtin_amdgcn_frexp_expf(__uint_as_float(top)) - 3, -127);
-  uint32_t word = 0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float a = ldexpf(fabsf(f[k]), -e);
-    uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.f);
-    c |= (__float_as_uint(f[k]) >> 28) & 8u;
-    word |= c << (4 * k);
-  }
-  codes[i] = finite ? word : 0u;
-  if ((i & 3) == 0) scales[i / 4] = static_cast<uint8_t>(finite ? e + 127 : 255);
 }
 
 template <int DT>
-__global__ __launch_bounds__(256) void mx_dequantize_kernel(uint16_t* __restrict__ y, int64_t ld,
-                                                            const uint32_t* __restrict__ codes,
-                                                            const uint8_t* __restrict__ scales,
-                                                            int64_t rows, int32_t h) {
-  const int64_t per_row = h / 8, total = rows * per_row;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int64_t row = i / per_row, at = i % per_row;
-  const uint32_t w = codes[i];
-  const float s = mx_scale(scales[i / 4]);
-  uint32_t out[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t e = word(mx_eight<SGMV_F16>(w, 1.f), k);
-    out[k] = Elem<DT>::pack(Elem<SGMV_F16>::lo(e) * s, Elem<SGMV_F16>::hi(e) * s);
+__device__ inline uint32_t mx_encode8(const uint4& v, float scale) {
+  uint32_t c = 0;
+  if constexpr (DT == SGMV_BF16) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, v.x), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, v.y), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, v.z), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, v.w), scale, 3);
+  } else {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2_t, v.x), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2_t, v.y), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2_t, v.z), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2_t, v.w), scale, 3);
   }
-  store_words<4>(y + row * ld + 8 * at, out);
+  return c;
+}
+
+// the larger of each 16-bit half
+__device__ inline uint32_t max_halves(uint32_t a, uint32_t b) {
+  typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                __builtin_bit_cast(u16x2_t, b)));
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(uint32_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales,
+                                                          const uint16_t* __restrict__ x, MxSpan S) {
+  constexpr uint32_t kMag = 0x7fff7fffu, kInf = DT == SGMV_BF16 ? 0x7f80u : 0x7c00u;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kMxPer) + threadIdx.x;
+  uint4 v[kMxPer];
+#pragma unroll
+  for (int u = 0; u < kMxPer; ++u) v[u] = ld16(x + S.at(min(i0 + 256 * u, S.pieces - 1)));
+#pragma unroll
+  for (int u = 0; u < kMxPer; ++u) {
+    const int64_t i = i0 + 256 * u;
+    uint32_t top = max_halves(max_halves(v[u].x & kMag, v[u].y & kMag), max_halves(v[u].z & kMag, v[u].w & kMag));
+    top = max(top & 0xffffu, top >> 16);
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 1)));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 2)));
+    const bool finite = top < kInf;
+    const uint32_t b = finite ? mx_scale_byte<DT>(top) : 255u;
+    const uint32_t c = mx_encode8<DT>(v[u], mx_scale(finite ? b : 127u));
+    if (i < S.pieces) {  // the pieces are a multiple of 4: a block's lanes go together
+      codes[i] = finite ? c : 0u;
+      if ((i & 3) == 0) scales[i / 4] = static_cast<uint8_t>(b);
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(uint16_t* __restrict__ y,
+                                                            const uint32_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, MxSpan S) {
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kMxPer) + threadIdx.x;
+  uint32_t w[kMxPer], b[kMxPer];
+#pragma unroll
+  for (int u = 0; u < kMxPer; ++u) {
+    const int64_t i = min(i0 + 256 * u, S.pieces - 1);
+    w[u] = codes[i];
+    b[u] = scales[i / 4];
+  }
+#pragma unroll
+  for (int u = 0; u < kMxPer; ++u) {
+    const int64_t i = i0 + 256 * u;
+    // exact in bfloat16; rounded to nearest even where float16 does not hold the value
+    const uint4 v = mx_eight<DT>(w[u], mx_scale(b[u]));
+    const uint32_t out[4] = {v.x, v.y, v.z, v.w};
+    if (i < S.pieces) store_words<4>(y + S.at(i), out);
+  }
+}
+
+inline MxSpan mx_span(int64_t rows, int32_t h, int64_t ld) {
+  return {rows * (h / 8), rows == 1 || ld == h ? 0 : h / 8, ld};
+}
+inline uint32_t mx_grid(const MxSpan& S) {
+  return static_cast<uint32_t>((S.pieces + 256 * kMxPer - 1) / (256 * kMxPer));
 }
 
 inline int check_mx_rows(int64_t rows, int32_t h, int64_t ld) {
@@ -95,12 +148,12 @@ extern "C" int sgmv_mx_quantize(hipStream_t stream, int32_t dtype, void* codes, 
       ranges_overlap(codes, elems / 2, scales, elems / 32))
     return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
-  const uint32_t grid = static_cast<uint32_t>((elems / 8 + 255) / 256);
+  const MxSpan S = mx_span(rows, h, ld_x);
   auto* c = static_cast<uint32_t*>(codes);
   auto* s = static_cast<uint8_t*>(scales);
   auto* p = static_cast<const uint16_t*>(x);
-  if (dtype == SGMV_F16) mx_quantize_kernel<SGMV_F16><<<grid, 256, 0, stream>>>(c, s, p, ld_x, rows, h);
-  else mx_quantize_kernel<SGMV_BF16><<<grid, 256, 0, stream>>>(c, s, p, ld_x, rows, h);
+  if (dtype == SGMV_F16) mx_quantize_kernel<SGMV_F16><<<mx_grid(S), 256, 0, stream>>>(c, s, p, S);
+  else mx_quantize_kernel<SGMV_BF16><<<mx_grid(S), 256, 0, stream>>>(c, s, p, S);
   return hip_status(hipGetLastError());
 }
 
@@ -116,12 +169,12 @@ extern "C" int sgmv_mx_dequantize(hipStream_t stream, int32_t dtype, void* y, in
   if (ranges_overlap(codes, elems / 2, y, y_bytes) || ranges_overlap(scales, elems / 32, y, y_bytes))
     return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
-  const uint32_t grid = static_cast<uint32_t>((elems / 8 + 255) / 256);
+  const MxSpan S = mx_span(rows, h, ld_y);
   auto* c = static_cast<const uint32_t*>(codes);
   auto* s = static_cast<const uint8_t*>(scales);
   auto* p = static_cast<uint16_t*>(y);
-  if (dtype == SGMV_F16) mx_dequantize_kernel<SGMV_F16><<<grid, 256, 0, stream>>>(p, ld_y, c, s, rows, h);
-  else mx_dequantize_kernel<SGMV_BF16><<<grid, 256, 0, stream>>>(p, ld_y, c, s, rows, h);
+  if (dtype == SGMV_F16) mx_dequantize_kernel<SGMV_F16><<<mx_grid(S), 256, 0, stream>>>(p, c, s, S);
+  else mx_dequantize_kernel<SGMV_BF16><<<mx_grid(S), 256, 0, stream>>>(p, c, s, S);
   return hip_status(hipGetLastError());
 }
 
