@@ -224,9 +224,8 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
     S.y = static_cast<uint16_t*>(y);
     S.ld_x = ld_x, S.ld_y = ld_y, S.w_group = static_cast<int64_t>(h_in) * h_out / 2;
     S.h_in = h_in, S.h_out = h_out;
-    const int64_t tiles = max_row_tiles(n, n_groups, starts, kSkinnyRows);
-    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, true>(stream, S, tiles)
-                                        : launch_skinny<SGMV_BF16, true>(stream, S, tiles));
+    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, true>(stream, S)
+                                        : launch_skinny<SGMV_BF16, true>(stream, S));
   }
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};

@@ -1,18 +1,21 @@
 // Products of a few rows per group: the form for decode batches, bound by streaming the weight.
 //
-// One workgroup makes 16 * CT output columns for at most 64 rows of one group.  Its 8
-// wavefronts take turns along the contracted dimension (128 bytes of every weight row at a
-// time, so the workgroup walks each row in whole lines), load weight pieces straight into
-// registers as first MFMA operands and the rows of x, which stay in the L2, as second ones, and
-// add their sums in LDS at the end, always in the same order.  No tile is staged: a weight
-// element is used once per row tile, so the LDS would only add a trip.
+// One workgroup makes 16 * CT output columns for at most 32 rows of one group.  Its
+// wavefronts take turns along the contracted dimension, a unit of 128 bytes of every weight row
+// at a time, so the workgroup walks each row in order.  Each wavefront streams its units
+// through a ring of its own in LDS, three units ahead, by direct loads whose lanes follow the
+// rows' bytes (8 lanes to a row's line); a load straight into the MFMA operand's lanes, one row
+// to a lane, kept the address unit busy four times as long and held the stream at 3 TB/s.  The
+// rows of x, few and in the L2, go straight to registers one unit ahead.  Nothing is shared
+// between wavefronts until they add their sums in LDS at the end, always in the same order.
 //
-// 4-bit weights: a lane loads one block (16 bytes) of a weight row and its scale.  The block's
-// four groups of 8 elements are four MFMA operands, with x taken at the same positions.
+// 4-bit weights: a unit is eight blocks of a row; a lane reads two (16 bytes each) and their
+// scales.  A block's four groups of 8 elements are four MFMA operands, with x taken at the same
+// positions.
 // bfloat16 holds every element times its scale exactly, so the scale goes in with the
-// conversion.  float16 does for scales 2^-23 .. 2^13; where a wavefront meets another one it
-// takes x apart into two bfloat16 (8 + 3 of its 11 bits) and runs that block as two exact
-// bfloat16 products.
+// conversion.  float16 does for scales 2^-23 .. 2^13 (and for blocks of zeros); a workgroup
+// that meets another one starts again with x taken apart into two bfloat16 (8 + 3 of its 11
+// bits), as two exact bfloat16 products.
 #pragma once
 
 #include "sgmv_rows.h"
@@ -31,7 +34,7 @@ struct SkinnyArgs {
   int32_t h_in, h_out;
 };
 
-constexpr int kSkinnyRows = 64, kSkinnyWaves = 8;
+constexpr int kSkinnyRows = 32;
 
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
@@ -60,8 +63,10 @@ __device__ inline uint4 mx_eight(uint32_t codes, float scale) {
   return v;
 }
 
-// float16 holds 0.5 .. 6 times the scale exactly
-__device__ inline bool f16_holds(uint32_t b) { return b - 104u <= 36u; }
+// float16 holds the block's 32 elements times its scale exactly
+__device__ inline bool f16_holds(uint32_t b, const uint4& codes) {
+  return b - 104u <= 36u || ((codes.x | codes.y | codes.z | codes.w) & 0x77777777u) == 0;
+}
 
 // 8 float16 values as the sum of two bfloat16 each: the upper 8 bits and what is left of them
 __device__ inline void f16_split(const uint4& v, uint4* hi, uint4* lo) {
@@ -80,126 +85,213 @@ __device__ inline void f16_split(const uint4& v, uint4* hi, uint4* lo) {
   *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-template <int DT, bool MX, int CT>
-struct Skinny {
-  static constexpr int KU = MX ? 128 : 64;   // contracted elements of a unit
-  static constexpr int XL = MX ? 4 : 2;      // x loads (MFMAs per column tile) of a unit
-  static constexpr int WL = MX ? 1 : 2;      // weight loads of a column tile and unit
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-  template <int MT>
-  static __device__ void run(const SkinnyArgs& A, const RowTile& t, int c0,
-                             float (*sums)[16][16 * CT + 4]) {
-    constexpr int UN = MT == 4 ? 1 : 2;      // units in flight
+typedef __attribute__((address_space(3))) void tile_lds_void;
+typedef __attribute__((address_space(1))) void tile_global_void;
+
+// 16 bytes per lane from src into LDS at dst + 16 * lane (dst the same for the wavefront)
+__device__ inline void to_lds(const char* src, u32x4_t* dst) {
+  __builtin_amdgcn_global_load_lds((tile_global_void*)src, (tile_lds_void*)dst, 16, 0, 0);
+}
+
+template <int I, int N, class F>
+__device__ __forceinline__ void tile_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    tile_for<I + 1, N>(f);
+  }
+}
+
+template <int DT, bool MX, int CT, int WAVES>
+struct Skinny {
+  static constexpr int KU = MX ? 256 : 64;   // contracted elements of a unit
+  static constexpr int XL = MX ? 8 : 2;      // 8-element pieces of a lane and unit
+  static constexpr int D = 4;                // units of the ring
+  struct Ring {
+    u32x4_t v[WAVES * CT * 128];             // [wavefront][column tile][row of 16][8 pieces]
+  };
+
+  // This wavefront's part of the products, in acc.  False where float16 did not hold a weight
+  // (never with SPLIT, the exact way for any scale).
+  template <int MT, bool SPLIT>
+  static __device__ __forceinline__ bool multiply_rows(const SkinnyArgs& A, const RowTile& t, int c0,
+                                                       f32x4_t (*acc)[CT], Ring& r0, Ring& r1, Ring& r2,
+                                                       Ring& r3) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
-    const int K = A.h_in;
-    // the element of a unit at which this lane's first piece starts
-    const int k_lane = MX ? 32 * kq : 8 * kq;
-    constexpr int k_step = MX ? 8 : 32;      // between its x pieces
+    const int K = A.h_in, row_bytes = MX ? K / 2 : 2 * K;
+    // x: the element of a unit at which this lane's first piece starts, and from one to the next
+    const int k_lane = MX ? 64 * kq : 8 * kq;
+    constexpr int k_step = MX ? 8 : 32;
     gptr<const uint16_t> xp[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
       xp[m] = global_ptr(A.x) + A.share.div(A.T.row(t.row0 + min(16 * m + l16, t.rows - 1))) * A.ld_x + k_lane;
-    gptr<const char> wp[CT];
+    // weights: lane l fetches a piece of row l / 8 of 8, the one that belongs in its slot (piece c
+    // of row q of 16 sits in slot c ^ ((q >> 1) & 7): no bank conflicts for the reads below)
+    const char* wp[CT][2];
+    int wk[2];
     gptr<const uint8_t> sp[CT];
 #pragma unroll
+    for (int h = 0; h < 2; ++h) wk[h] = 16 * ((lane & 7) ^ (((8 * h + lane / 8) >> 1) & 7));
+#pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const int64_t col = min(c0 + 16 * c + l16, A.h_out - 1);
       const char* base = A.w + t.g * A.w_group;
-      wp[c] = global_ptr(base) + (MX ? col * (K / 2) + 16 * kq : 2 * col * K + 16 * kq);
-      if (MX) sp[c] = global_ptr(A.scales) + t.g * (A.w_group / 16) + col * (K / 32) + kq;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        wp[c][h] = base + static_cast<int64_t>(min(c0 + 16 * c + 8 * h + lane / 8, A.h_out - 1)) * row_bytes + wk[h];
+      const int64_t col = min(c0 + 16 * c + l16, A.h_out - 1);
+      if (MX) sp[c] = global_ptr(A.scales) + t.g * (A.w_group / 16) + col * (K / 32);
     }
-    f32x4_t acc[MT][CT];
+    const char* const zeros = reinterpret_cast<const char*>(kZeros);
+    // this wavefront's units: w, w + WAVES, ...; n of them, the row's last one partial or whole
+    const int units = (K + KU - 1) / KU, n = (units - w + WAVES - 1) / WAVES;
+    bool held = true;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[m][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    uint4 xv[UN][MT][XL], wv[UN][CT][WL];
-    uint32_t sv[UN][CT];
-    // pieces past the row's end are zeros in both operands; their address is the row's start
-    auto load = [&](int u, int unit, bool masked) {
-      const int k0 = unit * KU;
+    // the i-th unit of this wavefront; past the row's end (and past the last unit) zeros
+    auto fetch = [&](Ring& to, int i) __attribute__((always_inline)) {
+      const int at = (w + i * WAVES) * 128;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
+      for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int i = 0; i < WL; ++i) {
-          const bool in = !masked || k0 + k_lane + i * 32 < K;
-          const int64_t off = MX ? k0 / 2 : 2 * (k0 + 32 * i);
-          const uint4 v = ld16((gptr<const uint16_t>)(wp[c] + (in ? off : -16 * kq)));
-          wv[u][c][i] = in ? v : zero4();
-        }
-        if (MX) {
-          const bool in = !masked || k0 + k_lane < K;
-          const uint32_t b = sp[c][in ? k0 / 32 : -kq];
-          sv[u][c] = in ? b : 127u;
-        }
+        for (int h = 0; h < 2; ++h)
+          to_lds(at + wk[h] < row_bytes ? wp[c][h] + at : zeros, &to.v[((w * CT + c) * 2 + h) * 64]);
+    };
+    struct Rows {
+      uint4 x[MT][XL];
+      uint32_t s[CT][2];
+    };
+    // the rows of x at the i-th unit, and the scales of this lane's two blocks of each column
+    auto rows_of = [&](Rows& R, int i, bool masked) __attribute__((always_inline)) {
+      const int k0 = (w + i * WAVES) * KU;
+      if constexpr (MX) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int b = k0 / 32 + 2 * kq + v;
+            const uint32_t s = sp[c][masked ? min(b, K / 32 - 1) : b];
+            R.s[c][v] = !masked || b < K / 32 ? s : 127u;
+          }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < XL; ++i) {
-          const bool in = !masked || k0 + k_lane + i * k_step < K;
-          const uint4 v = ld16(xp[m] + (in ? k0 + i * k_step : -k_lane));
-          xv[u][m][i] = in ? v : zero4();
+        for (int p = 0; p < XL; ++p) {
+          const bool in = !masked || k0 + k_lane + p * k_step < K;
+          const uint4 v = ld16(xp[m] + (in ? k0 + p * k_step : -k_lane));
+          R.x[m][p] = in ? v : zero4();
         }
     };
-    auto multiply = [&](int u) {
-      if constexpr (!MX) {
+    int at = (w * CT * 16 + l16) * 8, sw = (l16 >> 1) & 7;
+    int slot[2] = {at + ((MX ? 2 * kq : kq) ^ sw), at + ((MX ? 2 * kq + 1 : 4 + kq) ^ sw)};
+    asm("" : "+v"(slot[0]), "+v"(slot[1]));  // one lane offset: see the tiled product
+    auto multiply = [&](const Ring& from, const Rows& R) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < XL; ++i)
+      for (int c = 0; c < CT; ++c) {
+        u32x4_t wv[2];
 #pragma unroll
-          for (int c = 0; c < CT; ++c)
+        for (int v = 0; v < 2; ++v) wv[v] = from.v[slot[v] + c * 128];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(wv[u][c][i], xv[u][m][i], acc[m][c]);
-      } else {
-        bool fits = true;
-        if constexpr (DT == SGMV_F16) {
-          bool ok = true;
+        for (int v = 0; v < 2; ++v) {
+          const uint4 p = make_uint4(wv[v].x, wv[v].y, wv[v].z, wv[v].w);
+          if constexpr (!MX) {
 #pragma unroll
-          for (int c = 0; c < CT; ++c) ok &= f16_holds(sv[u][c]);
-          fits = __all(ok);
-        }
-        if (fits) {
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const float s = mx_scale(sv[u][c]);
+            for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(p, R.x[m][v], acc[m][c]);
+          } else {
+            const float s = mx_scale(R.s[c][v]);
+            if constexpr (DT == SGMV_F16 && !SPLIT) held &= f16_holds(R.s[c][v], p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint4 e = mx_eight<DT>(word(wv[u][c][0], i), s);
+              if constexpr (SPLIT) {
+                const uint4 e = mx_eight<SGMV_BF16>(word(p, i), s);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(e, xv[u][m][i], acc[m][c]);
-            }
-          }
-        } else {
+                for (int m = 0; m < MT; ++m) {
+                  uint4 hi, lo;
+                  f16_split(R.x[m][4 * v + i], &hi, &lo);
+                  acc[m][c] = Elem<SGMV_BF16>::mfma(e, hi, acc[m][c]);
+                  acc[m][c] = Elem<SGMV_BF16>::mfma(e, lo, acc[m][c]);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // few registers, not speed
+              } else {
+                const uint4 e = mx_eight<DT>(word(p, i), s);
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 hi, lo;
-              f16_split(xv[u][m][i], &hi, &lo);
-#pragma unroll
-              for (int c = 0; c < CT; ++c) {
-                const uint4 e = mx_eight<SGMV_BF16>(word(wv[u][c][0], i), mx_scale(sv[u][c]));
-                acc[m][c] = Elem<SGMV_BF16>::mfma(e, hi, acc[m][c]);
-                acc[m][c] = Elem<SGMV_BF16>::mfma(e, lo, acc[m][c]);
+                for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(e, R.x[m][4 * v + i], acc[m][c]);
               }
             }
+          }
         }
       }
     };
-    const int whole = K / KU, units = (K + KU - 1) / KU;
-    int u = w;
-    for (; u + (UN - 1) * kSkinnyWaves < whole; u += UN * kSkinnyWaves) {
-#pragma unroll
-      for (int i = 0; i < UN; ++i) load(i, u + i * kSkinnyWaves, false);
-#pragma unroll
-      for (int i = 0; i < UN; ++i) multiply(i);
+    auto ring = [&](auto k) __attribute__((always_inline)) -> Ring& {
+      constexpr int j = decltype(k)::value % D;
+      if constexpr (j == 0) return r0;
+      else if constexpr (j == 1) return r1;
+      else if constexpr (j == 2) return r2;
+      else return r3;
+    };
+    // Rounds of D units, one to a ring buffer.  Loads of one wavefront arrive in order, so a
+    // unit's weights are there once at most the loads behind them are in flight: those of three
+    // units and of the rows of the next.
+    constexpr int W_LOADS = 2 * CT, X_LOADS = MT * XL + (MX ? 2 * CT : 0);
+    tile_for<0, D - 1>([&](auto k) __attribute__((always_inline)) { fetch(ring(k), decltype(k)::value); });
+    if constexpr (MT == 1 && !SPLIT) {
+      Rows a, b;
+      const int whole = n - (K % KU != 0 && (units - 1) % WAVES == w);
+      if (n > 0) rows_of(a, 0, true);
+      auto step = [&](auto k, int i, bool masked) __attribute__((always_inline)) {
+        constexpr int j = decltype(k)::value;
+        Rows &now = j % 2 ? b : a, &next = j % 2 ? a : b;
+        rows_of(next, i + j + 1, masked);
+        fetch(ring(std::integral_constant<int, j + D - 1>{}), i + j + D - 1);
+        wait_loads<(D - 1) * W_LOADS + X_LOADS>();
+        multiply(ring(k), now);
+      };
+      int i = 0;
+      for (; i + D < whole; i += D)
+        tile_for<0, D>([&](auto k) __attribute__((always_inline)) { step(k, i, false); });
+      tile_for<0, D + 1>([&](auto k) __attribute__((always_inline)) {
+        if (i + decltype(k)::value < n) step(k, i, true);
+      });
+    } else {  // two units' rows do not fit the registers
+      Rows a;
+      for (int i = 0; i < n; i += D)
+        tile_for<0, D>([&](auto k) __attribute__((always_inline)) {
+          constexpr int j = decltype(k)::value;
+          if (i + j < n) {
+            rows_of(a, i + j, true);
+            fetch(ring(std::integral_constant<int, j + D - 1>{}), i + j + D - 1);
+            wait_loads<(D - 1) * W_LOADS>();
+            multiply(ring(k), a);
+          }
+        });
     }
-    for (; u < units; u += kSkinnyWaves) {
-      load(0, u, true);
-      multiply(0);
-    }
+    wait_loads<0>();  // the last loads into LDS land before it is used again
+    return held;
+  }
 
+  // at most N global loads of this wavefront are in flight
+  template <int N>
+  static __device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt range");
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  }
+
+  template <int MT>
+  static __device__ __forceinline__ void run(const SkinnyArgs& A, const RowTile& t, int c0, Ring& r0, Ring& r1,
+                                             Ring& r2, Ring& r3, float (*sums)[16][16 * CT + 4]) {
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
+    f32x4_t acc[MT][CT];
+    const bool held = multiply_rows<MT, false>(A, t, c0, acc, r0, r1, r2, r3);
+    if constexpr (MX && DT == SGMV_F16) {
+      if (!__syncthreads_and(held)) multiply_rows<MT, true>(A, t, c0, acc, r0, r1, r2, r3);
+    }
     // sums of the wavefronts, 16 rows at a time
     constexpr int COLS = 16 * CT;
 #pragma unroll
@@ -209,12 +301,12 @@ struct Skinny {
       for (int c = 0; c < CT; ++c)
         *reinterpret_cast<f32x4_t*>(&sums[w][l16][16 * c + 4 * kq]) = acc[m][c];
       __syncthreads();
-      for (int i = tid; i < 16 * COLS; i += 64 * kSkinnyWaves) {
+      for (int i = tid; i < 16 * COLS; i += 64 * WAVES) {
         const int r = i / COLS, c = i % COLS;
         if (16 * m + r < t.rows && c0 + c < A.h_out) {
           float s = 0.f;
 #pragma unroll
-          for (int v = 0; v < kSkinnyWaves; ++v) s += sums[v][r][c];
+          for (int v = 0; v < WAVES; ++v) s += sums[v][r][c];
           A.y[A.T.row(t.row0 + 16 * m + r) * A.ld_y + c0 + c] =
               static_cast<uint16_t>(Elem<DT>::pack(s, 0.f));
         }
@@ -223,9 +315,11 @@ struct Skinny {
   }
 };
 
-template <int DT, bool MX, int CT>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(SkinnyArgs A) {
-  __shared__ __attribute__((aligned(16))) float sums[kSkinnyWaves][16][16 * CT + 4];
+template <int DT, bool MX, int CT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyArgs A) {
+  using S = Skinny<DT, MX, CT, WAVES>;
+  __shared__ typename S::Ring r0, r1, r2, r3;
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][16][16 * CT + 4];
   const int ct = (A.h_out + 16 * CT - 1) / (16 * CT);
   const TileList list(A.T, kSkinnyRows);
   const int m = blockIdx.x / ct, c0 = (blockIdx.x - m * ct) * 16 * CT;
@@ -238,26 +332,28 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(SkinnyArgs A)
     }
     return;
   }
-  using S = Skinny<DT, MX, CT>;
-  if (t.rows <= 16) S::template run<1>(A, t, c0, sums);
-  else if (t.rows <= 32) S::template run<2>(A, t, c0, sums);
-  else S::template run<4>(A, t, c0, sums);
+  if (t.rows <= 16) S::template run<1>(A, t, c0, r0, r1, r2, r3, sums);
+  else S::template run<2>(A, t, c0, r0, r1, r2, r3, sums);
 }
 
-// column tiles of a workgroup: few enough for two workgroups to a CU where the product has
-// them, otherwise more, which share the reads of x
-template <int DT, bool MX>
+// Columns and wavefronts of a workgroup.  16-bit weights: 16 columns, 4 wavefronts (64 experts of
+// 4096 x 1024, about 45 of them met: 38 us for 64 rows; 40 with 8 wavefronts or 32 columns).
+// 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
+// (8 experts of 5120 x 13824: 93 us for 32 rows; 104 with 4 wavefronts, 124 with 16 columns), or
+// 16 columns and 8 wavefronts where that leaves most CUs without work.
+template <int DT, bool MX, int CT, int WAVES>
 hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A, int64_t row_tiles) {
-  constexpr int WIDE = MX ? 4 : 2;
-  const int wide = (A.h_out + 16 * WIDE - 1) / (16 * WIDE);
-  // row tiles that hold rows: at most the groups and the rows
-  if (row_tiles * wide >= 512) {
-    skinny_kernel<DT, MX, WIDE><<<static_cast<uint32_t>(row_tiles * wide), 64 * kSkinnyWaves, 0, s>>>(A);
-  } else {
-    const int64_t grid = row_tiles * ((A.h_out + 15) / 16);
-    skinny_kernel<DT, MX, 1><<<static_cast<uint32_t>(grid), 64 * kSkinnyWaves, 0, s>>>(A);
-  }
+  const int64_t grid = row_tiles * ((A.h_out + 16 * CT - 1) / (16 * CT));
+  skinny_kernel<DT, MX, CT, WAVES><<<static_cast<uint32_t>(grid), 64 * WAVES, 0, s>>>(A);
   return hipGetLastError();
+}
+
+template <int DT, bool MX>
+hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A) {
+  const int64_t row_tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, kSkinnyRows);
+  if constexpr (!MX) return launch_skinny<DT, MX, 1, 4>(s, A, row_tiles);
+  else if (row_tiles * (A.h_out / 32) >= 512) return launch_skinny<DT, MX, 2, 2>(s, A, row_tiles);
+  else return launch_skinny<DT, MX, 1, 8>(s, A, row_tiles);
 }
 
 }  // namespace sgmv_dev

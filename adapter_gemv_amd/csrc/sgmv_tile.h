@@ -53,16 +53,6 @@ enum Mode { kForward, kDx, kDw, kMxW, kMxBoth };
 
 typedef __attribute__((ext_vector_type(8))) int i32x8_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
-typedef __attribute__((address_space(3))) void tile_lds_void;
-typedef __attribute__((address_space(1))) void tile_global_void;
-
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
-
-// 16 bytes per lane from src into LDS at dst + 16 * lane (dst the same for the wavefront)
-__device__ inline void to_lds(const char* src, u32x4_t* dst) {
-  __builtin_amdgcn_global_load_lds((tile_global_void*)src, (tile_lds_void*)dst, 16, 0, 0);
-}
-
 // at most N (< 16) global loads of this wavefront are in flight, and every LDS access of it is
 // done; then the workgroup's barrier
 template <int N>
@@ -84,14 +74,6 @@ struct TileArgs {
   int32_t rows, cols, depth;          // dW: output rows; output columns; contracted bytes of a
                                       // row (kAlong) or contracted rows (kAcross)
 };
-
-template <int I, int N, class F>
-__device__ __forceinline__ void tile_for(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    tile_for<I + 1, N>(f);
-  }
-}
 
 // kAcross, tiles of B columns: pieces of 16 bytes between slabs, contracted rows of a slab
 constexpr int kSlab = 66;
