@@ -11,52 +11,75 @@ using namespace sgmv_host;
 namespace {
 
 // ------------------------------------------------------------------------------------
-// group tables: a stable counting sort by one workgroup
+// group tables: a stable counting sort in one launch
 // ------------------------------------------------------------------------------------
-// Bin G takes the rows of no group.  Each wavefront owns a contiguous run of rows (a multiple
-// of 64).  It counts them per bin in LDS, the counts are summed over (bin, wavefront) in that
-// order, and each wavefront then places its rows 64 at a time: a row's place is its bin's next
-// free one plus the number of lower lanes of the same bin, found by one ballot per bit of the
-// bin number.  All counts are integers, so the tables do not depend on timing.  One workgroup
-// bounds this by its own latency (about 64 rows per wavefront and 0.2 us), which the products
-// it precedes hide many times over; several workgroups would need a second launch.
+// Bin G takes the rows of no group.  A workgroup places a contiguous run of rows, each of its
+// wavefronts a contiguous part of it (a multiple of 64).  It counts them per bin in LDS, and the
+// rows before and behind its run (by itself, so that nothing is exchanged between workgroups);
+// sums over (bin, wavefront) in that order, behind the rows before the run, give each wavefront
+// its places.  It then places its rows 64 at a time: a row's place is its bin's next free one
+// plus the number of lower lanes of the same bin, found by one ballot per bit of the bin number.
+// All counts are integers, so the tables do not depend on timing.  What takes time is the
+// placing, one memory access for each row: 65 us for 32768 rows of 64 groups by one workgroup in
+// an early form, 27 with ids fetched eight at a time, and a few with one workgroup for 4096 rows.
 constexpr int kBinSlots = 8 * (kMaxGroups + 1) + 8;  // 16 wavefronts up to 512 groups, 8 above
+constexpr int kGroupRun = 4096;                      // rows of a workgroup, at least
+constexpr int kGroupMost = 64;                       // workgroups
 inline int group_waves(int G) { return 16 * (G + 1) <= kBinSlots ? 16 : 8; }
 
 __global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restrict__ ids, int32_t n,
                                                           int32_t G, int32_t* __restrict__ perm,
                                                           int32_t* __restrict__ starts) {
   __shared__ int bins[kBinSlots];  // [wavefront][G + 1]
+  __shared__ int before[kMaxGroups + 1], behind[kMaxGroups + 1];
   __shared__ int sums[16];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, waves = blockDim.x >> 6;
   const int B = G + 1;
   for (int i = tid; i < waves * B; i += blockDim.x) bins[i] = 0;
+  for (int i = tid; i < B; i += blockDim.x) before[i] = behind[i] = 0;
   __syncthreads();
-  const int run = ((n + waves - 1) / waves + 63) & ~63;
-  const int lo = min(n, w * run), hi = min(n, lo + run);
+  // 64-bit: the last workgroups' runs may start past n
+  const int run = ((n + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x) + 1023) & ~1023;
+  const int first = static_cast<int>(min<int64_t>(n, static_cast<int64_t>(blockIdx.x) * run));
+  const int last = static_cast<int>(min<int64_t>(n, static_cast<int64_t>(first) + run));
+  const int part = run / waves;  // a multiple of 64
+  const int lo = min(last, first + w * part), hi = min(last, lo + part);
   int* mine = bins + w * B;
   auto bin_of = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(G) ? id : G; };
   // ids come eight at a time: one trip to memory for 512 rows of the wavefront
   constexpr int U = 8;
   int id[U];
-  auto fetch = [&](int i0) {
+  auto fetch = [&](int i0, int step, int end) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) id[u] = ids[min(i0 + 64 * u + lane, hi - 1)];
+    for (int u = 0; u < U; ++u) id[u] = ids[min(i0 + step * u, end - 1)];
   };
   for (int i0 = lo; i0 < hi; i0 += 64 * U) {
-    fetch(i0);
+    fetch(i0 + lane, 64, hi);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + 64 * u + lane < hi) atomicAdd(&mine[bin_of(id[u])], 1);
   }
+  auto count = [&](int* where, int from, int to) {  // by the whole workgroup
+    const int step = blockDim.x;
+    for (int64_t i0 = from; i0 < to; i0 += step * U) {
+      fetch(static_cast<int>(i0) + tid, step, to);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + step * u + tid < to) atomicAdd(&where[bin_of(id[u])], 1);
+    }
+  };
+  count(before, 0, first);
+  count(behind, last, n);
   __syncthreads();
   // exclusive sums over bins, then over a bin's wavefronts
   int carry = 0;
   for (int b0 = 0; b0 < B; b0 += blockDim.x) {
     const int b = b0 + tid;
     int total = 0;
-    if (b < B)
+    if (b < B) {
+      total = before[b] + behind[b];
       for (int v = 0; v < waves; ++v) total += bins[v * B + b];
+    }
     const int incl = wave_scan(total);
     if (lane == 63) sums[w] = incl;
     __syncthreads();
@@ -64,7 +87,8 @@ __global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restr
     for (int v = 0; v < w; ++v) at += sums[v];
     for (int v = 0; v < waves; ++v) carry += sums[v];
     if (b < B) {
-      starts[b] = at;
+      if (blockIdx.x == 0) starts[b] = at;
+      at += before[b];
       for (int v = 0; v < waves; ++v) {
         const int c = bins[v * B + b];
         bins[v * B + b] = at;
@@ -76,7 +100,7 @@ __global__ __launch_bounds__(1024) void group_rows_kernel(const int32_t* __restr
   const int bits = 32 - __builtin_clz(static_cast<uint32_t>(G));
   volatile int* next = mine;
   for (int i0 = lo; i0 < hi; i0 += 64 * U) {
-    fetch(i0);
+    fetch(i0 + lane, 64, hi);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + 64 * u + lane;
@@ -105,9 +129,6 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
   return stride % 8 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
 }
 
-// rows per group, on average, below which the streaming kernel runs
-constexpr int kSkinnyMost = 24;
-
 template <int DT, int B, int WR, int WC>
 hipError_t launch_dw(hipStream_t s, const TileArgs& A) {
   const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
@@ -130,11 +151,12 @@ hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
 
 extern "C" int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n, int32_t n_groups,
                                int32_t* perm, int32_t* starts) {
-  if (n < 0 || n_groups < 1) return SGMV_ERR_SHAPE;
+  if (n < 0 || n > kMaxGroupRows || n_groups < 1) return SGMV_ERR_SHAPE;
   if (n_groups > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
   if (!starts || (n > 0 && (!ids || !perm))) return SGMV_ERR_NULL;
   if (int st = check_device()) return st;
-  group_rows_kernel<<<1, 64 * group_waves(n_groups), 0, stream>>>(ids, n, n_groups, perm, starts);
+  const int grid = std::min(kGroupMost, std::max(1, n / kGroupRun));
+  group_rows_kernel<<<grid, 64 * group_waves(n_groups), 0, stream>>>(ids, n, n_groups, perm, starts);
   return hip_status(hipGetLastError());
 }
 
@@ -156,7 +178,7 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
     return SGMV_ERR_ALIAS;
   if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
-  if (n / n_groups < kSkinnyMost) {
+  if (few_rows(n, n_groups, h_in, h_out, false)) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -164,8 +186,7 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
     S.w = static_cast<const char*>(W);
     S.y = static_cast<uint16_t*>(y);
     S.ld_x = ld_x, S.ld_y = ld_y, S.w_group = 2 * W_stride, S.h_in = h_in, S.h_out = h_out;
-    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, false>(stream, S)
-                                        : launch_skinny<SGMV_BF16, false>(stream, S));
+    return hip_status(launch_skinny<false, false>(dtype, stream, S));
   }
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};

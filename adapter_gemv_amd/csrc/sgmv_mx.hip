@@ -11,8 +11,6 @@ using namespace sgmv_host;
 namespace {
 
 constexpr int kMxBlock = 32;
-// rows per group, on average, below which the streaming kernel runs
-constexpr int kMxSkinnyMost = 48;
 
 // Both kernels move every byte once and are bound by that: four lanes to a block of 32, 8
 // elements (16 bytes of values, 4 of codes) each, so a wavefront's accesses are whole lines, and
@@ -214,7 +212,7 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
-  if (n / n_groups < kMxSkinnyMost) {
+  if (few_rows(n, n_groups, h_in, h_out, true)) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -224,8 +222,7 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
     S.y = static_cast<uint16_t*>(y);
     S.ld_x = ld_x, S.ld_y = ld_y, S.w_group = static_cast<int64_t>(h_in) * h_out / 2;
     S.h_in = h_in, S.h_out = h_out;
-    return hip_status(dtype == SGMV_F16 ? launch_skinny<SGMV_F16, true>(stream, S)
-                                        : launch_skinny<SGMV_BF16, true>(stream, S));
+    return hip_status(launch_skinny<true, false>(dtype, stream, S));
   }
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};
@@ -255,6 +252,19 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
   if (ranges_overlap(y, y_bytes, x_codes, elems / 2) || ranges_overlap(y, y_bytes, x_scales, elems / 32))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
+  if (few_rows(n, n_groups, h_in, h_out, true)) {
+    SkinnyArgs S{};
+    S.T = {starts, perm, n, n_groups};
+    S.share = share_of(share);
+    S.x = static_cast<const uint16_t*>(x_codes);
+    S.x_scales = static_cast<const uint8_t*>(x_scales);
+    S.w = static_cast<const char*>(W_codes);
+    S.scales = static_cast<const uint8_t*>(W_scales);
+    S.y = static_cast<uint16_t*>(y);
+    S.ld_y = ld_y, S.w_group = static_cast<int64_t>(h_in) * h_out / 2;
+    S.h_in = h_in, S.h_out = h_out;
+    return hip_status(launch_skinny<true, true>(dtype, stream, S));
+  }
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};
   A.share = share_of(share);

@@ -101,6 +101,7 @@ struct TileList {
 namespace sgmv_host {
 
 constexpr int kMaxGroups = SGMV_MAX_GROUPS;
+constexpr int32_t kMaxGroupRows = 1 << 30;  // row numbers plus a workgroup's stride stay int32
 
 inline sgmv_dev::Share share_of(int32_t share) {
   if (share == 1) return {0u, ~0u};
@@ -112,7 +113,7 @@ inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7
 // tables and group count of a grouped call; 0 when fine (n may be 0)
 inline int check_groups(int32_t n, int32_t G, int32_t share, const int32_t* starts,
                         const int32_t* perm) {
-  if (n < 0 || G < 1 || share < 1) return SGMV_ERR_SHAPE;
+  if (n < 0 || n > kMaxGroupRows || G < 1 || share < 1) return SGMV_ERR_SHAPE;
   if (G > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n) * share > INT32_MAX) return SGMV_ERR_SHAPE;
   if (!starts && G != 1) return SGMV_ERR_NULL;

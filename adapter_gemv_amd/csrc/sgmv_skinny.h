@@ -15,8 +15,12 @@
 // bfloat16 holds every element times its scale exactly, so the scale goes in with the
 // conversion.  float16 does for scales 2^-23 .. 2^13 (and for blocks of zeros); a workgroup
 // that meets another one starts again with x taken apart into two bfloat16 (8 + 3 of its 11
-// bits), as two exact bfloat16 products.
+// bits), as two exact bfloat16 products.  With x in 4 bits too, both sides are bfloat16.
 #pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "sgmv_rows.h"
 
@@ -25,7 +29,8 @@ namespace sgmv_dev {
 struct SkinnyArgs {
   RowTab T;
   Share share;
-  const uint16_t* x;
+  const uint16_t* x;         // 16-bit rows, or codes
+  const uint8_t* x_scales;
   const char* w;             // 16-bit weights or codes
   const uint8_t* scales;
   uint16_t* y;
@@ -63,9 +68,9 @@ __device__ inline uint4 mx_eight(uint32_t codes, float scale) {
   return v;
 }
 
-// float16 holds the block's 32 elements times its scale exactly
-__device__ inline bool f16_holds(uint32_t b, const uint4& codes) {
-  return b - 104u <= 36u || ((codes.x | codes.y | codes.z | codes.w) & 0x77777777u) == 0;
+// float16 holds these codes (or'd together) times the scale exactly
+__device__ inline bool f16_holds(uint32_t b, uint32_t codes) {
+  return b - 104u <= 36u || (codes & 0x77777777u) == 0;
 }
 
 // 8 float16 values as the sum of two bfloat16 each: the upper 8 bits and what is left of them
@@ -103,8 +108,11 @@ __device__ __forceinline__ void tile_for(F&& f) {
   }
 }
 
-template <int DT, bool MX, int CT, int WAVES>
+// XM: x in 4 bits (its rows dense), DT the type of y alone
+template <int DT, bool MX, bool XM, int CT, int WAVES>
 struct Skinny {
+  static_assert(MX || !XM, "");
+  static constexpr int CTYPE = XM ? SGMV_BF16 : DT;  // of the products
   static constexpr int KU = MX ? 256 : 64;   // contracted elements of a unit
   static constexpr int XL = MX ? 8 : 2;      // 8-element pieces of a lane and unit
   static constexpr int D = 4;                // units of the ring
@@ -124,9 +132,13 @@ struct Skinny {
     const int k_lane = MX ? 64 * kq : 8 * kq;
     constexpr int k_step = MX ? 8 : 32;
     gptr<const uint16_t> xp[MT];
+    gptr<const uint8_t> xs[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      xp[m] = global_ptr(A.x) + A.share.div(A.T.row(t.row0 + min(16 * m + l16, t.rows - 1))) * A.ld_x + k_lane;
+    for (int m = 0; m < MT; ++m) {
+      const int row = A.share.div(A.T.row(t.row0 + min(16 * m + l16, t.rows - 1)));
+      xp[m] = global_ptr(A.x) + (XM ? row * (static_cast<int64_t>(K) / 4) : row * A.ld_x) + k_lane / (XM ? 4 : 1);
+      if (XM) xs[m] = global_ptr(A.x_scales) + row * (static_cast<int64_t>(K) / 32);
+    }
     // weights: lane l fetches a piece of row l / 8 of 8, the one that belongs in its slot (piece c
     // of row q of 16 sits in slot c ^ ((q >> 1) & 7): no bank conflicts for the reads below)
     const char* wp[CT][2];
@@ -162,8 +174,8 @@ struct Skinny {
           to_lds(at + wk[h] < row_bytes ? wp[c][h] + at : zeros, &to.v[((w * CT + c) * 2 + h) * 64]);
     };
     struct Rows {
-      uint4 x[MT][XL];
-      uint32_t s[CT][2];
+      uint4 x[MT][XM ? 2 : XL];
+      uint32_t s[CT][2], xs[MT][2];
     };
     // the rows of x at the i-th unit, and the scales of this lane's two blocks of each column
     auto rows_of = [&](Rows& R, int i, bool masked) __attribute__((always_inline)) {
@@ -179,17 +191,35 @@ struct Skinny {
           }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (XM) {
 #pragma unroll
-        for (int p = 0; p < XL; ++p) {
-          const bool in = !masked || k0 + k_lane + p * k_step < K;
-          const uint4 v = ld16(xp[m] + (in ? k0 + p * k_step : -k_lane));
-          R.x[m][p] = in ? v : zero4();
+          for (int v = 0; v < 2; ++v) {
+            const int b = k0 / 32 + 2 * kq + v;
+            const bool in = !masked || b < K / 32;
+            const uint4 c = ld16(xp[m] + (in ? k0 / 4 + 8 * v : -(k_lane / 4)));
+            const uint32_t s = xs[m][in ? b : 0];
+            R.x[m][v] = in ? c : zero4();
+            R.xs[m][v] = in ? s : 127u;
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < XL; ++p) {
+            const bool in = !masked || k0 + k_lane + p * k_step < K;
+            const uint4 v = ld16(xp[m] + (in ? k0 + p * k_step : -k_lane));
+            R.x[m][p] = in ? v : zero4();
+          }
         }
+      }
     };
     int at = (w * CT * 16 + l16) * 8, sw = (l16 >> 1) & 7;
     int slot[2] = {at + ((MX ? 2 * kq : kq) ^ sw), at + ((MX ? 2 * kq + 1 : 4 + kq) ^ sw)};
     asm("" : "+v"(slot[0]), "+v"(slot[1]));  // one lane offset: see the tiled product
+    // the p-th piece of a row
+    auto piece = [&](const Rows& R, int m, int p) __attribute__((always_inline)) {
+      if constexpr (XM) return mx_eight<SGMV_BF16>(word(R.x[m][p / 4], p % 4), mx_scale(R.xs[m][p / 4]));
+      else return R.x[m][p];
+    };
     auto multiply = [&](const Ring& from, const Rows& R) __attribute__((always_inline)) {
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
@@ -204,7 +234,7 @@ struct Skinny {
             for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(p, R.x[m][v], acc[m][c]);
           } else {
             const float s = mx_scale(R.s[c][v]);
-            if constexpr (DT == SGMV_F16 && !SPLIT) held &= f16_holds(R.s[c][v], p);
+            if constexpr (CTYPE == SGMV_F16 && !SPLIT) held &= f16_holds(R.s[c][v], p.x | p.y | p.z | p.w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if constexpr (SPLIT) {
@@ -218,9 +248,9 @@ struct Skinny {
                 }
                 __builtin_amdgcn_sched_barrier(0);  // few registers, not speed
               } else {
-                const uint4 e = mx_eight<DT>(word(p, i), s);
+                const uint4 e = mx_eight<CTYPE>(word(p, i), s);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(e, R.x[m][4 * v + i], acc[m][c]);
+                for (int m = 0; m < MT; ++m) acc[m][c] = Elem<CTYPE>::mfma(e, piece(R, m, 4 * v + i), acc[m][c]);
               }
             }
           }
@@ -237,7 +267,7 @@ struct Skinny {
     // Rounds of D units, one to a ring buffer.  Loads of one wavefront arrive in order, so a
     // unit's weights are there once at most the loads behind them are in flight: those of three
     // units and of the rows of the next.
-    constexpr int W_LOADS = 2 * CT, X_LOADS = MT * XL + (MX ? 2 * CT : 0);
+    constexpr int W_LOADS = 2 * CT, X_LOADS = MT * (XM ? 4 : XL) + (MX ? 2 * CT : 0);
     tile_for<0, D - 1>([&](auto k) __attribute__((always_inline)) { fetch(ring(k), decltype(k)::value); });
     if constexpr (MT == 1 && !SPLIT) {
       Rows a, b;
@@ -289,7 +319,7 @@ struct Skinny {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
     f32x4_t acc[MT][CT];
     const bool held = multiply_rows<MT, false>(A, t, c0, acc, r0, r1, r2, r3);
-    if constexpr (MX && DT == SGMV_F16) {
+    if constexpr (MX && CTYPE == SGMV_F16) {
       if (!__syncthreads_and(held)) multiply_rows<MT, true>(A, t, c0, acc, r0, r1, r2, r3);
     }
     // sums of the wavefronts, 16 rows at a time
@@ -315,9 +345,9 @@ struct Skinny {
   }
 };
 
-template <int DT, bool MX, int CT, int WAVES>
+template <int DT, bool MX, bool XM, int CT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyArgs A) {
-  using S = Skinny<DT, MX, CT, WAVES>;
+  using S = Skinny<DT, MX, XM, CT, WAVES>;
   __shared__ typename S::Ring r0, r1, r2, r3;
   __shared__ __attribute__((aligned(16))) float sums[WAVES][16][16 * CT + 4];
   const int ct = (A.h_out + 16 * CT - 1) / (16 * CT);
@@ -340,20 +370,46 @@ __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyAr
 // 4096 x 1024, about 45 of them met: 38 us for 64 rows; 40 with 8 wavefronts or 32 columns).
 // 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
 // (8 experts of 5120 x 13824: 93 us for 32 rows; 104 with 4 wavefronts, 124 with 16 columns), or
-// 16 columns and 8 wavefronts where that leaves most CUs without work.
-template <int DT, bool MX, int CT, int WAVES>
+// 16 columns and 8 wavefronts where that leaves CUs without work (5120 x 13824, 16 rows: 33 and
+// 41 us; 4096 x 4096: 9.1 and 8.9).
+template <int DT, bool MX, bool XM, int CT, int WAVES>
 hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A, int64_t row_tiles) {
   const int64_t grid = row_tiles * ((A.h_out + 16 * CT - 1) / (16 * CT));
-  skinny_kernel<DT, MX, CT, WAVES><<<static_cast<uint32_t>(grid), 64 * WAVES, 0, s>>>(A);
+  skinny_kernel<DT, MX, XM, CT, WAVES><<<static_cast<uint32_t>(grid), 64 * WAVES, 0, s>>>(A);
   return hipGetLastError();
 }
 
-template <int DT, bool MX>
-hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A) {
+template <bool MX, bool XM>
+hipError_t launch_skinny(int32_t dtype, hipStream_t s, const SkinnyArgs& A) {
   const int64_t row_tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, kSkinnyRows);
-  if constexpr (!MX) return launch_skinny<DT, MX, 1, 4>(s, A, row_tiles);
-  else if (row_tiles * (A.h_out / 32) >= 512) return launch_skinny<DT, MX, 2, 2>(s, A, row_tiles);
-  else return launch_skinny<DT, MX, 1, 8>(s, A, row_tiles);
+  const bool f16 = dtype == SGMV_F16;
+  if constexpr (!MX)
+    return f16 ? launch_skinny<SGMV_F16, false, false, 1, 4>(s, A, row_tiles)
+               : launch_skinny<SGMV_BF16, false, false, 1, 4>(s, A, row_tiles);
+  else if (row_tiles * (A.h_out / 32) >= 256)
+    return f16 ? launch_skinny<SGMV_F16, true, XM, 2, 2>(s, A, row_tiles)
+               : launch_skinny<SGMV_BF16, true, XM, 2, 2>(s, A, row_tiles);
+  else
+    return f16 ? launch_skinny<SGMV_F16, true, XM, 1, 8>(s, A, row_tiles)
+               : launch_skinny<SGMV_BF16, true, XM, 1, 8>(s, A, row_tiles);
+}
+
+// Whether few rows meet each weight, so that streaming beats tiles: the smaller of two estimates,
+// in microseconds.  Both were fitted to 1 to 64 groups of 8 to 256 rows (weights 4096 x 1024 to
+// 5120 x 13824).  Streaming takes 0.38 to 0.5 us (16-bit) or 0.23 to 0.38 us (4-bit) for a million
+// weights and row tile, the less where the rows are at most 16.  Tiles of 128 x 128 take 0.56 us
+// (4-bit: 0.8 us) for 64 contracted elements and round of the card, and for 16-bit weights no less
+// than the stream at 4.3 TB/s.  Of groups only the mean size is known: each is taken to end in
+// half a tile.
+inline bool few_rows(int32_t n, int32_t G, int32_t h_in, int32_t h_out, bool mx) {
+  const double met = std::min(n, G), weights = 1e-6 * h_in * h_out;
+  const auto tiles = [&](double B) { return G == 1 ? std::ceil(n / B) : std::max(met, n / B + met / 2); };
+  const bool small = n <= 16 * met;
+  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.23 : 0.38) : (small ? 0.38 : 0.5));
+  const double tiles128 = tiles(128) * std::ceil(h_out / 128.0), steps = h_in / 64.0;
+  const double tiled = mx ? 0.8 * steps * std::max(1.0, tiles128 / 320)
+                          : std::max(0.56 * steps * std::max(1.0, tiles128 / 512), met * weights * 2 / 4.3);
+  return stream < tiled;
 }
 
 }  // namespace sgmv_dev

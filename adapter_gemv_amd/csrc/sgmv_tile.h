@@ -24,9 +24,9 @@
 //
 // Weights in 4 bits against 16-bit rows (kMxW): a stage of a weight row is 32 bytes of codes
 // (kCodes); a lane reads 16 codes, one half for each half of the stage, and converts them with
-// their scale to the 16-bit operand, exactly in bfloat16.  For float16 rows the product runs in
-// bfloat16 too, the rows taken apart into two bfloat16 parts (8 + 3 of their 11 bits), since
-// float16 does not hold every element times its scale.
+// their scale to the 16-bit operand, exactly in bfloat16.  float16 holds an element times its
+// scale for scales 2^-23 .. 2^13 (and blocks of zeros); a tile that meets another one starts
+// again in bfloat16, the rows taken apart into two bfloat16 parts (8 + 3 of their 11 bits).
 // Both sides in 4 bits (kMxBoth): the fragments are the 16x16x128 scaled MFMA's operands, whose
 // blocks of 32 are the format's own; the scale bytes go through LDS in the order in which its
 // byte selectors take them.
@@ -177,6 +177,8 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   for (int i = 0; i < NR; ++i)
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  bool held = true;  // kMxW, float16: every weight so far, exactly
 
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
   const char* const cbase = A.c + (DW ? 0 : static_cast<int64_t>(t.g) * A.c_group);
@@ -362,8 +364,10 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   constexpr bool SPREAD = BR == 256;
   constexpr int PER = NC > NQ ? NC / NQ : 1, FROM = NQ - NC / PER;  // column fragments of a step
   auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb, const typename C::MxScales& sb,
-                   typename C::RBuf& rn, typename C::CBuf& cn, typename C::MxScales& sn,
-                   int s) __attribute__((always_inline)) {
+                   typename C::RBuf& rn, typename C::CBuf& cn, typename C::MxScales& sn, int s,
+                   auto split) __attribute__((always_inline)) {
+    constexpr bool SPLIT = decltype(split)::value;
+    constexpr int WT = SPLIT ? SGMV_BF16 : DT;  // kMxW: type of the converted weights
     uint4 cv[2][NC], rv[2];
     uint32_t rs[NR / 2], cs[NC / 2];
     if constexpr (M == kMxW) {
@@ -374,9 +378,11 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         codes[j] = reinterpret_cast<const u32x2_t*>(cb.v)[co[0] + 64 * j];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const float f = mx_scale(from[j]);
-        cv[0][j] = mx_eight<SGMV_BF16>(codes[j].x, f);
-        cv[1][j] = mx_eight<SGMV_BF16>(codes[j].y, f);
+        const uint32_t b = from[j];
+        const float f = mx_scale(b);
+        if constexpr (DT == SGMV_F16 && !SPLIT) held &= f16_holds(b, codes[j].x | codes[j].y);
+        cv[0][j] = mx_eight<WT>(codes[j].x, f);
+        cv[1][j] = mx_eight<WT>(codes[j].y, f);
       }
     } else {
 #pragma unroll
@@ -404,7 +410,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         for (int j = 0; j < PER; ++j) cv[1][(n - FROM) * PER + j] = cfrag(cb, (n - FROM) * PER + j, 1);
       }
       uint4 hi, lo;
-      if constexpr (M == kMxW && DT == SGMV_F16) f16_split(rv[n & 1], &hi, &lo);
+      if constexpr (SPLIT) f16_split(rv[n & 1], &hi, &lo);
       tile_for<0, NC>([&](auto col) __attribute__((always_inline)) {
         constexpr int j = decltype(col)::value;
         if constexpr (M == kMxBoth) {
@@ -413,7 +419,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
           const i32x8_t bv = {int(b.x), int(b.y), int(b.z), int(b.w), 0, 0, 0, 0};
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
               av, bv, acc[i][j], 4, 4, (j % 2) * 2 + u, cs[j / 2], (i % 2) * 2 + u, rs[i / 2]);
-        } else if constexpr (M == kMxW && DT == SGMV_F16) {
+        } else if constexpr (SPLIT) {
           acc[i][j] = Elem<SGMV_BF16>::mfma(cv[u][j], hi, acc[i][j]);
           acc[i][j] = Elem<SGMV_BF16>::mfma(cv[u][j], lo, acc[i][j]);
         } else {
@@ -428,7 +434,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   // No branch inside the loop, which keeps the accumulators where they are: stages go in pairs
   // (an odd count's last one is zeros), or in sixes where the columns have three buffers, with
   // the remainder behind the loop; what is fetched behind the end is zeros.
-  if (nst > 0) {
+  auto all_stages = [&](auto split) __attribute__((always_inline)) {
     rows_of(0);
     fetch_scales(0);
     if constexpr (DW) {
@@ -441,9 +447,9 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
     if constexpr (DC == 2) {
       for (int s = 0; s < nst; s += 2) {
         wait_stage<0>();
-        stage(rb0, cb0, sb0, rb1, cb1, sb1, s);
+        stage(rb0, cb0, sb0, rb1, cb1, sb1, s, split);
         wait_stage<0>();
-        stage(rb1, cb1, sb1, rb0, cb0, sb0, s + 1);
+        stage(rb1, cb1, sb1, rb0, cb0, sb0, s + 1, split);
       }
     } else {
       __shared__ typename C::CBuf cb2;
@@ -454,7 +460,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         typename C::CBuf &c = k % 3 == 0 ? cb0 : k % 3 == 1 ? cb1 : cb2;
         typename C::CBuf &cn = k % 3 == 0 ? cb2 : k % 3 == 1 ? cb0 : cb1;
         wait_stage<CI>();
-        stage(r, c, sb0, rn, cn, sb0, s + k);
+        stage(r, c, sb0, rn, cn, sb0, s + k, split);
       };
       int s = 0;
       for (; s + 6 <= nst; s += 6) tile_for<0, 6>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
@@ -462,7 +468,19 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         if (s + decltype(k)::value < nst) nth(k, s);
       });
     }
-    wait_stage<0>();  // the last loads into LDS land before the workgroup can end
+    wait_stage<0>();  // the last loads into LDS land before it is used again or given back
+  };
+  if (nst > 0) {
+    all_stages(std::false_type{});
+    if constexpr (M == kMxW && DT == SGMV_F16) {
+      if (!__syncthreads_and(held)) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int j = 0; j < NC; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        all_stages(std::true_type{});
+      }
+    }
   }
 
   // lane (l16, kq): row l16 of a fragment, columns 8 * (kq >> 1) .. + 7 of column tile

@@ -447,7 +447,7 @@ int sgmv_lora_add_host_ids_noalloc(hipStream_t stream, int32_t dtype, void* y, i
  * n rows one group in caller order: a dense product.
  *
  * These calls need no workspace.  Their errors are those of the other calls: SGMV_ERR_SHAPE
- * (also for share < 1 and for products of more than 2^31 - 1 tiles), SGMV_ERR_ALIGNMENT,
+ * (also for n > 2^30, share < 1, n * share >= 2^31 and products of more than 2^31 - 1 tiles), SGMV_ERR_ALIGNMENT,
  * SGMV_ERR_NULL, SGMV_ERR_UNSUPPORTED (dtype; n_groups above SGMV_MAX_GROUPS),
  * SGMV_ERR_ALIAS (an output overlaps an input), SGMV_ERR_HIP.
  */

@@ -103,7 +103,8 @@ def check_all(torch, x, dy, W, ids, share, dtype, what, pad=0):
 # group tables
 # --------------------------------------------------------------------------------------
 @pytest.mark.parametrize("n,E", [(0, 3), (1, 1), (5, 1), (63, 2), (64, 7), (65, 64), (1000, 65),
-                                 (1023, 300), (5000, 512), (5000, 513), (20011, 1024), (40000, 8)])
+                                 (1023, 300), (5000, 512), (5000, 513), (20011, 1024), (40000, 8),
+                                 (8191, 3), (8192, 3), (300001, 77)])
 def test_group_rows(torch, n, E):
     import adapter_gemv_amd as sgmv
     rng = np.random.default_rng(n + E)
@@ -125,6 +126,65 @@ def test_group_rows(torch, n, E):
 # --------------------------------------------------------------------------------------
 # products
 # --------------------------------------------------------------------------------------
+def spread(got, ref_of, outs, what, dtype, depth):
+    """Blocks of rows against the oracle, so that a large result needs little memory."""
+    for lo in range(0, outs, 512):
+        rows = np.arange(lo, min(outs, lo + 512))
+        close(got(rows), *ref_of(rows), depth, dtype, f"{what} rows {lo}..")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,share,E,depth,wide", [(4200, 1, 3, 200, 4096), (2300, 2, 2, 392, 4000),
+                                                     (4097, 1, 1, 72, 4104)])
+def test_enough_work_for_the_largest_tiles(torch, dtype, rows, share, E, depth, wide):
+    """Products that fill the card with 256 x 256 tiles: ragged groups, rows of no group,
+    contracted lengths that end inside a stage, an odd and an even number of stages."""
+    import adapter_gemv_amd as sgmv
+    n = rows * share
+    rng = np.random.default_rng(7)
+    ids = rng.choice(np.arange(-1, E), n, p=np.r_[0.05, np.full(E, 0.95 / E)])
+    groups = sgmv.group_rows(torch.tensor(ids, dtype=torch.int32, device="cuda"), E)
+    x, dy, W, _ = problem(torch, 17, dtype, rows, share, E, depth, wide, ids=ids, pad=8)
+    y = sgmv.group_matmul(torch.empty(n, wide, dtype=x.dtype, device="cuda"), x, W, groups)
+    X, D, Wd = f64(x), f64(dy), f64(W)
+
+    def forward(rows_):
+        ref, mag = np.zeros((len(rows_), wide)), np.zeros((len(rows_), wide))
+        for g in range(E):
+            m = ids[rows_] == g
+            a = X[rows_[m] // share]
+            ref[m], mag[m] = a @ Wd[g].T, np.abs(a) @ np.abs(Wd[g]).T
+        return ref, mag
+
+    spread(lambda r: f64(y[torch.tensor(r, device="cuda")]), forward, n, "y", dtype, depth)
+    # dx: the contracted dimension is W's rows, the wide one its columns
+    Wt = W.transpose(1, 2).contiguous()
+    z = torch.randn(n, depth, device="cuda").to(x.dtype) * depth ** -0.5
+    dx = sgmv.group_matmul_dx(torch.empty(n, wide, dtype=x.dtype, device="cuda"), z, Wt, groups)
+    Z, Wt64 = f64(z), f64(Wt)
+
+    def backward(rows_):
+        ref, mag = np.zeros((len(rows_), wide)), np.zeros((len(rows_), wide))
+        for g in range(E):
+            m = ids[rows_] == g
+            ref[m], mag[m] = Z[rows_[m]] @ Wt64[g], np.abs(Z[rows_[m]]) @ np.abs(Wt64[g])
+        return ref, mag
+
+    spread(lambda r: f64(dx[torch.tensor(r, device="cuda")]), backward, n, "dx", dtype, depth)
+    # dW of a wide weight from few rows: the first ones
+    few = 2 * depth // share * share
+    x2, _ = padded(torch, few // share, wide, x.dtype, 8, torch.Generator(device="cuda").manual_seed(3))
+    ids2 = rng.integers(-1, E, few)
+    g2 = sgmv.group_rows(torch.tensor(ids2, dtype=torch.int32, device="cuda"), E)
+    dW = sgmv.group_matmul_dw(torch.empty(E, wide, wide, dtype=x.dtype, device="cuda"), x2, dy[:few], g2)
+    X2, D2 = f64(x2), D[:few]
+    for g in range(E):
+        m = np.flatnonzero(ids2 == g)
+        a = X2[m // share]
+        spread(lambda r: f64(dW[g, torch.tensor(r, device="cuda")]),
+               lambda r: (D2[m][:, r].T @ a, np.abs(D2[m][:, r]).T @ np.abs(a)), wide, f"dW {g}", dtype, few)
+
+
 SHAPES = [
     # x rows, share, E, K, N
     (1, 1, 1, 8, 8), (1, 2, 4, 64, 32), (1, 4, 64, 1024, 264), (2, 1, 3, 72, 40),

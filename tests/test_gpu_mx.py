@@ -180,7 +180,32 @@ def test_products(torch, shape, dtype):
     check(torch, x, q, ids, share, dtype, "mx")
 
 
-@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("K", [256, 544, 96])
+def test_enough_work_for_the_largest_tiles(torch, dtype, K):
+    """Products that fill the card with 256 x 256 tiles, ragged groups, blocks that end inside a
+    stage; every row against the oracle, 512 at a time."""
+    import adapter_gemv_amd as sgmv
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(22)
+    rows, E, N = 4300, 3, 4104
+    x = torch.randn(rows, K, generator=gen, device="cuda").to(_dt(torch, dtype))
+    q = weights(torch, gen, E, N, K, dtype)
+    q.scales[0, 7] = 90                                  # float16 does not hold these weights
+    ids = torch.randint(-1, E, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    groups, ids_h = sgmv.group_rows(ids, E), ids.cpu().numpy()
+    Wd = G.mx_decode(q.codes.cpu().numpy(), q.scales.cpu().numpy())
+    for both in (False, True):
+        y = sgmv.mx_matmul(torch.empty(rows, N, dtype=x.dtype, device="cuda"),
+                           sgmv.mx_quantize(x) if both else x, q, groups)
+        X = G.mx_decode(*G.mx_encode(f64(x))) if both else f64(x)
+        for lo in range(0, rows, 512):
+            part = slice(lo, min(rows, lo + 512))
+            ref, mag = G.group_matmul(X[part], Wd, ids_h[part])
+            close(f64(y[part]), ref, mag, K, dtype, f"both {both} rows {lo}..")
+
+
+@pytest.mark.parametrize("rows", [3, 40, 200, 3000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("low", [1, 60, 118, 140])
 def test_scales_of_any_size(torch, rows, dtype, low):

@@ -28,6 +28,8 @@ MXQ = dict(stream=None, dtype=1, y=Y, ld_y=512, x=X, x_scales=S + (1 << 30), sha
 COMMON = [
     ("dtype", dict(dtype=2), _lib.ERR_UNSUPPORTED),
     ("n<0", dict(n=-1), _lib.ERR_SHAPE),
+    ("n", dict(n=(1 << 30) + 1), _lib.ERR_SHAPE),
+    ("tiles", dict(n=1 << 30, h_in=1 << 22, h_out=1 << 22), _lib.ERR_SHAPE),
     ("no group", dict(n_groups=0), _lib.ERR_SHAPE),
     ("groups", dict(n_groups=1025), _lib.ERR_UNSUPPORTED),
     ("starts null", dict(starts=None), _lib.ERR_NULL),
@@ -103,6 +105,7 @@ def test_mx_refusals():
 def test_group_rows_refusals():
     L = _lib.lib()
     assert L.sgmv_group_rows(None, T, -1, 4, Y, S) == _lib.ERR_SHAPE
+    assert L.sgmv_group_rows(None, T, (1 << 30) + 1, 4, Y, S) == _lib.ERR_SHAPE
     assert L.sgmv_group_rows(None, T, 5, 0, Y, S) == _lib.ERR_SHAPE
     assert L.sgmv_group_rows(None, T, 5, 1025, Y, S) == _lib.ERR_UNSUPPORTED
     assert L.sgmv_group_rows(None, None, 5, 4, Y, S) == _lib.ERR_NULL
