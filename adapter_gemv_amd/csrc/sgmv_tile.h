@@ -99,7 +99,8 @@ struct Tile {
   static_assert(NR % 4 == 0 && NR >= NC, "runs of row fragments");
   static_assert(!DW || BR == BC, "dW shares its row indices between the operands");
   static_assert(M != kMxBoth || (BR == BC && BR + BC == TH), "one thread to a row's or column's scales");
-  static_assert(M != kMxW || 2 * BC == TH, "one thread to a column's block");
+  static constexpr int SB = M == kMxW ? 2 * BC / TH : 1;      // kMxW: a thread's scale bytes of a stage
+  static_assert(M != kMxW || SB * TH == 2 * BC, "the same number of scale bytes for each thread");
 
   // scale bytes as a lane takes them.  kMxBoth: [lane group][wavefront tile][row of 16]
   // [fragment][half] of the rows, then of the columns; kMxW: [half][wavefront tile][row of 16]
@@ -279,8 +280,8 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
                 : A.c_scale + (static_cast<int64_t>(t.g) * A.cols + min(c0 + q, A.cols - 1)) * blocks;
   } else if constexpr (M == kMxW) {
     blocks = depth / 64;
-    const int q = tid % BC, half = tid / BC;
-    sto = ((half * WC + q / (16 * NC)) * 16 + q % 16) * NC + q / 16 % NC;
+    const int q = tid % BC;  // and block tid / BC of the stage's two, or both
+    sto = ((tid / BC * WC + q / (16 * NC)) * 16 + q % 16) * NC + q / 16 % NC;
     if (depth)
       sp = A.c_scale + (static_cast<int64_t>(t.g) * A.cols + min(c0 + q, A.cols - 1)) * blocks;
   }
@@ -296,9 +297,12 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         sv[i / 4] |= (8 * s + i < blocks ? b : 127u) << (8 * (i & 3));
       }
     } else if constexpr (M == kMxW) {
-      const int k = 2 * s + tid / BC;
-      const uint32_t b = global_ptr(sp)[min(k, blocks - 1)];
-      sv[0] = k < blocks ? b : 127u;
+#pragma unroll
+      for (int h = 0; h < C::SB; ++h) {
+        const int k = 2 * s + tid / BC + h;
+        const uint32_t b = global_ptr(sp)[min(k, blocks - 1)];
+        sv[h] = k < blocks ? b : 127u;
+      }
     }
   };
   auto store_scales = [&](typename C::MxScales& to) {  // no branch: see the loop below
@@ -308,7 +312,8 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
         *reinterpret_cast<uint16_t*>(to.b + sto + k * (WR * NR * 32)) =
             static_cast<uint16_t>(__builtin_amdgcn_perm(sv[1], sv[0], k | (4 + k) << 8));
     } else if constexpr (M == kMxW) {
-      to.b[sto] = static_cast<uint8_t>(sv[0]);
+#pragma unroll
+      for (int h = 0; h < C::SB; ++h) to.b[sto + h * BC] = static_cast<uint8_t>(sv[h]);
     }
   };
   // Fragment reads.  Each address is one lane offset, made here, plus a constant: the compiler
@@ -361,7 +366,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   // 913 TFLOP/s at once, 871 spread out).  The fences keep the compiler from hoisting more reads
   // than there are registers for.
   constexpr int NQ = NR / 4;
-  constexpr bool SPREAD = BR == 256;
+  constexpr bool SPREAD = BC == 256;
   constexpr int PER = NC > NQ ? NC / NQ : 1, FROM = NQ - NC / PER;  // column fragments of a step
   auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb, const typename C::MxScales& sb,
                    typename C::RBuf& rn, typename C::CBuf& cn, typename C::MxScales& sn, int s,
@@ -521,13 +526,25 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
 // 8 groups of 256 to 1024 rows).  A group's last tile is taken to be half full.
 constexpr int kCus = 256;
 
-#ifdef TILE_BIG
-inline bool big_tiles(double, double) { return TILE_BIG == 0; }
-#else
 inline bool big_tiles(double tiles256, double tiles128) {
   return std::ceil(tiles256 / kCus) <= 0.7 * std::ceil(tiles128 / (2 * kCus));
 }
-#endif
+
+// With 4-bit weights there is room for 128 rows x 256 columns, two workgroups to a CU: half as much
+// of a group's last tile is empty, and each weight is still turned into 16 bits only once for 128
+// rows.  For 64 stages (4096 contracted elements) a CU takes 118 us for a tile of 256 x 256, 67 us
+// for one of 128 x 256 and 54 us for one of 128 x 128, whether one or two of the latter run
+// together.  Measured with each: 8 groups of 192 rows, 4096 x 8192, 126 us against 165 with
+// 128 x 128; of 256 rows, 133 against 127 with 256 x 256; 64 groups of 384 rows, 4096 x 1024, 225
+// against 257; one of 1024 rows, 4096 x 4096, 69 against 57 with 128 x 128, of 2048 rows 77
+// against 106.
+template <typename F>
+int mx_tile(F tiles) {
+  const auto time = [](double one, double n) { return one * std::ceil(n / kCus); };
+  const double big = time(1, tiles(256, 256)), half = time(0.57, tiles(128, 256)),
+               small = time(0.46, tiles(128, 128));
+  return big <= std::min(half, small) ? 0 : half < small ? 1 : 2;
+}
 
 template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
 hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
@@ -540,11 +557,24 @@ hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
 template <Mode M, bool WHOLE = true>
 hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
   const auto columns = [&](int BC) { return (A.cols + BC - 1) / BC; };
-  const auto expected = [&](int B) {
-    return (static_cast<double>(A.T.n) / B + 0.5 * std::min(A.T.n, A.T.G)) * columns(B);
+  const auto expected = [&](int BR, int BC) {
+    const double n = A.T.n;
+    return (A.T.starts ? n / BR + 0.5 * std::min(A.T.n, A.T.G) : std::ceil(n / BR)) * columns(BC);
   };
   const bool f16 = dtype == SGMV_F16;
-  if (big_tiles(expected(256), expected(128))) {
+  bool big = false;
+  if constexpr (M == kMxW) {
+    const int tile = mx_tile(expected);
+    big = tile == 0;
+    if (tile == 1) {
+      const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 128) * columns(256);
+      return f16 ? launch_tile<SGMV_F16, M, 128, 256, 1, 4, WHOLE>(s, tiles, A)
+                 : launch_tile<SGMV_BF16, M, 128, 256, 1, 4, WHOLE>(s, tiles, A);
+    }
+  } else {
+    big = big_tiles(expected(256, 256), expected(128, 128));
+  }
+  if (big) {
     const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 256) * columns(256);
     return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A)
                : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A);

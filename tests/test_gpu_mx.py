@@ -205,6 +205,30 @@ def test_enough_work_for_the_largest_tiles(torch, dtype, K):
             close(f64(y[part]), ref, mag, K, dtype, f"both {both} rows {lo}..")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("E,K", [(0, 96), (0, 512), (7, 160), (40, 288)])
+def test_enough_work_for_half_of_the_largest_tiles(torch, dtype, E, K):
+    """Products of about one round of 128 x 256 tiles, from one group of whole tiles to 40 ragged
+    ones with rows of none; every row against the oracle, 512 at a time."""
+    import adapter_gemv_amd as sgmv
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(23)
+    rows, N = 1100, 7000 if E == 0 else 5000 if E == 7 else 1544
+    x = torch.randn(rows, K, generator=gen, device="cuda").to(_dt(torch, dtype))
+    q = weights(torch, gen, max(E, 1), N, K, dtype)
+    if E == 0:
+        q = sgmv.MxTensor(q.codes[0], q.scales[0])
+    ids = torch.randint(-1, E, (rows,), generator=gen, device="cuda", dtype=torch.int32) if E else None
+    groups = sgmv.group_rows(ids, E) if E else None
+    Wd = G.mx_decode(q.codes.cpu().numpy(), q.scales.cpu().numpy())
+    y = sgmv.mx_matmul(torch.full((rows, N), float("nan"), dtype=x.dtype, device="cuda"), x, q, groups)
+    for lo in range(0, rows, 512):
+        part = slice(lo, min(rows, lo + 512))
+        ref, mag = G.group_matmul(f64(x[part]), Wd if E else Wd[None],
+                                  ids[part].cpu().numpy() if E else np.zeros(part.stop - lo, np.int32))
+        close(f64(y[part]), ref, mag, K, dtype, f"rows {lo}..")
+
+
 @pytest.mark.parametrize("rows", [3, 40, 200, 3000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("low", [1, 60, 118, 140])
