@@ -20,8 +20,8 @@ namespace {
 // its places.  It then places its rows 64 at a time: a row's place is its bin's next free one
 // plus the number of lower lanes of the same bin, found by one ballot per bit of the bin number.
 // All counts are integers, so the tables do not depend on timing.  What takes time is the
-// placing, one memory access for each row: 65 us for 32768 rows of 64 groups by one workgroup in
-// an early form, 27 with ids fetched eight at a time, and a few with one workgroup for 4096 rows.
+// placing, one memory access for each row.  Whole calls with 32768 rows of 64 groups: 32 us by one
+// workgroup, 27 with its ids fetched eight at a time, 12 with one workgroup for 4096 rows.
 constexpr int kBinSlots = 8 * (kMaxGroups + 1) + 8;  // 16 wavefronts up to 512 groups, 8 above
 constexpr int kGroupRun = 4096;                      // rows of a workgroup, at least
 constexpr int kGroupMost = 64;                       // workgroups
