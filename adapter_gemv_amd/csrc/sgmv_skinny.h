@@ -5,13 +5,14 @@
 // at a time, so the workgroup walks each row in order.  Each wavefront streams its units
 // through a ring of its own in LDS, three units ahead, by direct loads whose lanes follow the
 // rows' bytes (8 lanes to a row's line); loads straight into the MFMA operand's lanes, one row to
-// a lane, took 98 us where this form takes 93 (4-bit, 8 experts of 5120 x 13824, 32 rows).  The
+// a lane, took 98 us where the ring took 93 (4-bit, 8 experts of 5120 x 13824, 32 rows).  The
 // rows of x, few and in the L2, go straight to registers one unit ahead.  Nothing is shared
 // between wavefronts until they add their sums in LDS at the end, always in the same order.
 //
-// 4-bit weights: a unit is eight blocks of a row; a lane reads two (16 bytes each) and their
-// scales.  A block's four groups of 8 elements are four MFMA operands, with x taken at the same
-// positions.
+// 4-bit weights: a unit is eight blocks of a row, each the operand of one MFMA: a lane takes 8
+// elements of every block, as in the 16-bit form, so that 4 lanes read 64 bytes of x side by side
+// (two whole blocks to a lane, and 16 bytes of x out of every 128 for each load: 10 % slower), and
+// the scales of four units are fetched at once and dealt out between lanes.
 // bfloat16 holds every element times its scale exactly, so the scale goes in with the
 // conversion.  float16 does for scales 2^-23 .. 2^13 (and for blocks of zeros); a workgroup
 // that meets another one starts again with x taken apart into two bfloat16 (8 + 3 of its 11
@@ -47,6 +48,12 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 // 2^(b - 127); NaN for 255
 __device__ inline float mx_scale(uint32_t b) {
   return __uint_as_float(b == 255 ? 0x7fc00000u : (b ? b << 23 : 1u << 22));
+}
+
+// byte `at` of a word of scales, for mx_eight: of its scale the conversion reads the exponent's
+// bits alone, as the format means them (0 is 2^-127, 255 NaN), so what stands beside them may stay
+__device__ inline float mx_scale_at(uint32_t scales, int at) {
+  return __uint_as_float(at == 3 ? scales >> 1 : scales << (23 - 8 * at));
 }
 
 // 8 codes of a word times a scale, as 16-bit elements (exact in bfloat16; in float16 for scales
@@ -129,21 +136,22 @@ struct Skinny {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
     const int K = A.h_in, row_bytes = MX ? K / 2 : 2 * K;
     // x: the element of a unit at which this lane's first piece starts, and from one to the next
-    const int k_lane = MX ? 64 * kq : 8 * kq;
-    constexpr int k_step = MX ? 8 : 32;
+    const int k_lane = 8 * kq;
     gptr<const uint16_t> xp[MT];
     gptr<const uint8_t> xs[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = A.share.div(A.T.row(t.row0 + min(16 * m + l16, t.rows - 1)));
       xp[m] = global_ptr(A.x) + (XM ? row * (static_cast<int64_t>(K) / 4) : row * A.ld_x) + k_lane / (XM ? 4 : 1);
-      if (XM) xs[m] = global_ptr(A.x_scales) + row * (static_cast<int64_t>(K) / 32);
+      if constexpr (XM) {
+        const int of = A.share.div(A.T.row(t.row0 + min(16 * m + (lane / 2) % 16, t.rows - 1)));
+        xs[m] = global_ptr(A.x_scales) + of * (static_cast<int64_t>(K) / 32);
+      }
     }
     // weights: lane l fetches a piece of row l / 8 of 8, the one that belongs in its slot (piece c
     // of row q of 16 sits in slot c ^ ((q >> 1) & 7): no bank conflicts for the reads below)
     const char* wp[CT][2];
     int wk[2];
-    gptr<const uint8_t> sp[CT];
 #pragma unroll
     for (int h = 0; h < 2; ++h) wk[h] = 16 * ((lane & 7) ^ (((8 * h + lane / 8) >> 1) & 7));
 #pragma unroll
@@ -152,9 +160,11 @@ struct Skinny {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         wp[c][h] = base + static_cast<int64_t>(min(c0 + 16 * c + 8 * h + lane / 8, A.h_out - 1)) * row_bytes + wk[h];
-      const int64_t col = min(c0 + 16 * c + l16, A.h_out - 1);
-      if (MX) sp[c] = global_ptr(A.scales) + t.g * (A.w_group / 16) + col * (K / 32);
     }
+    // scales: lane l fetches those of column l / 2 (of row (l / 2) % 16 of x) for a whole round,
+    // those of its units 0 and 1 in even lanes and 2 and 3 in odd ones
+    gptr<const uint8_t> sp = global_ptr(A.scales);
+    if (MX) sp += t.g * (A.w_group / 16) + static_cast<int64_t>(min(c0 + lane / 2 % (16 * CT), A.h_out - 1)) * (K / 32);
     const char* const zeros = reinterpret_cast<const char*>(kZeros);
     // this wavefront's units: w, w + WAVES, ...; n of them, the row's last one partial or whole
     const int units = (K + KU - 1) / KU, n = (units - w + WAVES - 1) / WAVES;
@@ -173,85 +183,127 @@ struct Skinny {
         for (int h = 0; h < 2; ++h)
           to_lds(at + wk[h] < row_bytes ? wp[c][h] + at : zeros, &to.v[((w * CT + c) * 2 + h) * 64]);
     };
+    using Piece = std::conditional_t<XM, uint32_t, uint4>;
     struct Rows {
-      uint4 x[MT][XM ? 2 : XL];
-      uint32_t s[CT][2], xs[MT][2];
+      Piece x[MT][XL];
     };
-    // the rows of x at the i-th unit, and the scales of this lane's two blocks of each column
-    auto rows_of = [&](Rows& R, int i, bool masked) __attribute__((always_inline)) {
-      const int k0 = (w + i * WAVES) * KU;
+    struct Scales {
+      uint32_t w[2][2], x[MT][2][2];  // [unit][first or last four blocks]
+    };
+    // a unit's eight scales from block b0; past the row's end 1
+    auto eight_scales = [&](uint32_t (&to)[2], gptr<const uint8_t> from, int b0, bool masked)
+        __attribute__((always_inline)) {
+      if (!masked || K % KU == 0) {
+        __builtin_memcpy(to, (const uint8_t*)(from + (masked ? min(b0, K / 32 - 8) : b0)), 8);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          to[h] = 0;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int at = b0 + 4 * h + v;
+            const uint32_t one = from[min(at, K / 32 - 1)];
+            to[h] |= (at < K / 32 ? one : 127u) << (8 * v);
+          }
+        }
+      }
+    };
+    // the scales of the round that starts with this wavefront's i-th unit
+    auto scales_of = [&](Scales& S, int i, bool masked) __attribute__((always_inline)) {
       if constexpr (MX) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int u = 0; u < 2; ++u) {
+          const int b0 = (w + (i + 2 * (lane & 1) + u) * WAVES) * 8;
+          eight_scales(S.w[u], sp, b0, masked);
+          if constexpr (XM)
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int b = k0 / 32 + 2 * kq + v;
-            const uint32_t s = sp[c][masked ? min(b, K / 32 - 1) : b];
-            R.s[c][v] = !masked || b < K / 32 ? s : 127u;
-          }
+            for (int m = 0; m < MT; ++m) eight_scales(S.x[m][u], xs[m], b0, masked);
+        }
       }
+    };
+    // the rows of x at the i-th unit
+    auto rows_of = [&](Rows& R, int i, bool masked) __attribute__((always_inline)) {
+      const int k0 = (w + i * WAVES) * KU;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if constexpr (XM) {
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int b = k0 / 32 + 2 * kq + v;
-            const bool in = !masked || b < K / 32;
-            const uint4 c = ld16(xp[m] + (in ? k0 / 4 + 8 * v : -(k_lane / 4)));
-            const uint32_t s = xs[m][in ? b : 0];
-            R.x[m][v] = in ? c : zero4();
-            R.xs[m][v] = in ? s : 127u;
-          }
-        } else {
-#pragma unroll
-          for (int p = 0; p < XL; ++p) {
-            const bool in = !masked || k0 + k_lane + p * k_step < K;
-            const uint4 v = ld16(xp[m] + (in ? k0 + p * k_step : -k_lane));
+        for (int p = 0; p < XL; ++p) {
+          const bool in = !masked || k0 + k_lane + 32 * p < K;
+          const int at = in ? k0 + 32 * p : -k_lane;
+          if constexpr (XM) {
+            const uint32_t v = *reinterpret_cast<gptr<const uint32_t>>(xp[m] + at / 4);
+            R.x[m][p] = in ? v : 0u;
+          } else {
+            const uint4 v = ld16(xp[m] + at);
             R.x[m][p] = in ? v : zero4();
           }
         }
       }
     };
-    int at = (w * CT * 16 + l16) * 8, sw = (l16 >> 1) & 7;
-    int slot[2] = {at + ((MX ? 2 * kq : kq) ^ sw), at + ((MX ? 2 * kq + 1 : 4 + kq) ^ sw)};
-    asm("" : "+v"(slot[0]), "+v"(slot[1]));  // one lane offset: see the tiled product
-    // the p-th piece of a row
-    auto piece = [&](const Rows& R, int m, int p) __attribute__((always_inline)) {
-      if constexpr (XM) return mx_eight<SGMV_BF16>(word(R.x[m][p / 4], p % 4), mx_scale(R.xs[m][p / 4]));
-      else return R.x[m][p];
+    // 32-bit words of a ring: this lane's in the p-th piece (4-bit) or its two pieces (16-bit)
+    const int at = (w * CT * 16 + l16) * 8, sw = (l16 >> 1) & 7;
+    int slot[MX ? 8 : 2];
+#pragma unroll
+    for (int p = 0; p < (MX ? 8 : 2); ++p) {
+      slot[p] = MX ? (at + (p ^ sw)) * 4 + kq : (at + ((4 * p + kq) ^ sw)) * 4;
+      asm("" : "+v"(slot[p]));  // one lane offset: see the tiled product
+    }
+    // the eight scales of entry e (a column, or a row of x) at the round's unit j
+    auto entry = [&](uint32_t (&to)[2], const uint32_t (&of)[2][2], int e, int j) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) to[h] = __builtin_amdgcn_ds_bpermute(4 * (2 * e + (j >> 1)), of[j & 1][h]);
     };
-    auto multiply = [&](const Ring& from, const Rows& R) __attribute__((always_inline)) {
+    auto multiply = [&](const Ring& from, const Rows& R, const Scales& S, int unit) __attribute__((always_inline)) {
+      const uint32_t* const words = reinterpret_cast<const uint32_t*>(from.v);
+      if constexpr (!MX) {
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        u32x4_t wv[2];
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) wv[v] = from.v[slot[v] + c * 128];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint4 p = make_uint4(wv[v].x, wv[v].y, wv[v].z, wv[v].w);
-          if constexpr (!MX) {
+          for (int v = 0; v < 2; ++v) {
+            const u32x4_t wv = *reinterpret_cast<const u32x4_t*>(&words[slot[v] + c * 512]);
+            const uint4 p = make_uint4(wv.x, wv.y, wv.z, wv.w);
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[m][c] = Elem<DT>::mfma(p, R.x[m][v], acc[m][c]);
-          } else {
-            const float s = mx_scale(R.s[c][v]);
-            if constexpr (CTYPE == SGMV_F16 && !SPLIT) held &= f16_holds(R.s[c][v], p.x | p.y | p.z | p.w);
+          }
+      } else {
+        uint32_t ws[CT][2], rs[MT][2], codes[CT][XL];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (SPLIT) {
-                const uint4 e = mx_eight<SGMV_BF16>(word(p, i), s);
+        for (int p = 0; p < XL; ++p)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  uint4 hi, lo;
-                  f16_split(R.x[m][4 * v + i], &hi, &lo);
-                  acc[m][c] = Elem<SGMV_BF16>::mfma(e, hi, acc[m][c]);
-                  acc[m][c] = Elem<SGMV_BF16>::mfma(e, lo, acc[m][c]);
-                }
-                __builtin_amdgcn_sched_barrier(0);  // few registers, not speed
-              } else {
-                const uint4 e = mx_eight<CTYPE>(word(p, i), s);
+          for (int c = 0; c < CT; ++c) codes[c][p] = words[slot[p] + c * 512];
+        __builtin_amdgcn_sched_barrier(0);  // all of them first: one at a time, each was waited for
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[m][c] = Elem<CTYPE>::mfma(e, piece(R, m, 4 * v + i), acc[m][c]);
+        for (int c = 0; c < CT; ++c) entry(ws[c], S.w, 16 * c + l16, unit);
+        if constexpr (XM)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) entry(rs[m], S.x[m], l16, unit);
+#pragma unroll
+        for (int p = 0; p < XL; ++p) {
+          uint4 xv[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if constexpr (XM) xv[m] = mx_eight<SGMV_BF16>(R.x[m][p], mx_scale_at(rs[m][p / 4], p % 4));
+            else xv[m] = R.x[m][p];
+          }
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const uint32_t code = codes[c][p];
+            const float s = mx_scale_at(ws[c][p / 4], p % 4);
+            if constexpr (CTYPE == SGMV_F16 && !SPLIT) held &= f16_holds(ws[c][p / 4] >> (8 * (p % 4)) & 255u, code);
+            if constexpr (SPLIT) {
+              const uint4 e = mx_eight<SGMV_BF16>(code, s);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                uint4 hi, lo;
+                f16_split(xv[m], &hi, &lo);
+                acc[m][c] = Elem<SGMV_BF16>::mfma(e, hi, acc[m][c]);
+                acc[m][c] = Elem<SGMV_BF16>::mfma(e, lo, acc[m][c]);
               }
+              __builtin_amdgcn_sched_barrier(0);  // few registers, not speed
+            } else {
+              const uint4 e = mx_eight<CTYPE>(code, s);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) acc[m][c] = Elem<CTYPE>::mfma(e, xv[m], acc[m][c]);
             }
           }
         }
@@ -267,8 +319,11 @@ struct Skinny {
     // Rounds of D units, one to a ring buffer.  Loads of one wavefront arrive in order, so a
     // unit's weights are there once at most the loads behind them are in flight: those of three
     // units and of the rows of the next.
-    constexpr int W_LOADS = 2 * CT, X_LOADS = MT * (XM ? 4 : XL) + (MX ? 2 * CT : 0);
+    static_assert(D == 4, "scales of a round");
+    constexpr int W_LOADS = 2 * CT, X_LOADS = MT * XL;
     tile_for<0, D - 1>([&](auto k) __attribute__((always_inline)) { fetch(ring(k), decltype(k)::value); });
+    Scales sn, sl;  // of this round and of the next
+    scales_of(sn, 0, true);
     if constexpr (MT == 1 && !SPLIT) {
       Rows a, b;
       const int whole = n - (K % KU != 0 && (units - 1) % WAVES == w);
@@ -276,29 +331,37 @@ struct Skinny {
       auto step = [&](auto k, int i, bool masked) __attribute__((always_inline)) {
         constexpr int j = decltype(k)::value;
         Rows &now = j % 2 ? b : a, &next = j % 2 ? a : b;
+        if constexpr (j == 0) scales_of(sl, i + D, masked);
+        if constexpr (j == D) sn = sl;
         rows_of(next, i + j + 1, masked);
         fetch(ring(std::integral_constant<int, j + D - 1>{}), i + j + D - 1);
         wait_loads<(D - 1) * W_LOADS + X_LOADS>();
-        multiply(ring(k), now);
+        multiply(ring(k), now, sn, j % D);
       };
+      constexpr int LAST = MX ? 2 * D : D + 1;  // rounds of whole units leave at most so many
       int i = 0;
-      for (; i + D < whole; i += D)
+      for (; i + LAST <= whole; i += D) {
         tile_for<0, D>([&](auto k) __attribute__((always_inline)) { step(k, i, false); });
-      tile_for<0, D + 1>([&](auto k) __attribute__((always_inline)) {
+        sn = sl;
+      }
+      tile_for<0, LAST>([&](auto k) __attribute__((always_inline)) {
         if (i + decltype(k)::value < n) step(k, i, true);
       });
     } else {  // two units' rows do not fit the registers
       Rows a;
-      for (int i = 0; i < n; i += D)
+      for (int i = 0; i < n; i += D) {
+        scales_of(sl, i + D, true);
         tile_for<0, D>([&](auto k) __attribute__((always_inline)) {
           constexpr int j = decltype(k)::value;
           if (i + j < n) {
             rows_of(a, i + j, true);
             fetch(ring(std::integral_constant<int, j + D - 1>{}), i + j + D - 1);
             wait_loads<(D - 1) * W_LOADS>();
-            multiply(ring(k), a);
+            multiply(ring(k), a, sn, j);
           }
         });
+        sn = sl;
+      }
     }
     wait_loads<0>();  // the last loads into LDS land before it is used again
     return held;
@@ -311,6 +374,7 @@ struct Skinny {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if constexpr (MX) __builtin_amdgcn_sched_barrier(0);  // a unit's use of its scales stays behind its wait
   }
 
   template <int MT>
@@ -369,7 +433,8 @@ __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyAr
 // Columns and wavefronts of a workgroup.  16-bit weights: 16 columns, 4 wavefronts (64 experts of
 // 4096 x 1024, 32 rows: 38 us; 40 with 8 wavefronts, 44 with 32 columns).
 // 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
-// (8 experts of 5120 x 13824: 93 us for 32 rows; 104 with 4 wavefronts, 124 with 16 columns), or
+// (8 experts of 5120 x 13824, 32 rows, in the first form: 93 us; 104 with 4 wavefronts, 124 with 16
+// columns; the call is now at 89), or
 // 16 columns and 8 wavefronts where that leaves CUs without work (5120 x 13824, 16 rows: 33 and
 // 41 us; 4096 x 4096: 9.1 and 8.9).
 template <int DT, bool MX, bool XM, int CT, int WAVES>
@@ -396,7 +461,7 @@ hipError_t launch_skinny(int32_t dtype, hipStream_t s, const SkinnyArgs& A) {
 
 // Whether few rows meet each weight, so that streaming beats tiles: the smaller of two estimates,
 // in microseconds.  Both were fitted to 1 to 64 groups of 8 to 256 rows (weights 4096 x 1024 to
-// 5120 x 13824).  Streaming takes 0.38 to 0.5 us (16-bit) or 0.23 to 0.38 us (4-bit) for a million
+// 5120 x 13824).  Streaming takes 0.38 to 0.5 us (16-bit) or 0.17 to 0.26 us (4-bit) for a million
 // weights and row tile, the less where the rows are at most 16.  Tiles of 128 x 128 take 0.56 us
 // (4-bit: 0.8 us) for 64 contracted elements and round of the card, and for 16-bit weights no less
 // than the stream at 4.3 TB/s.  Of groups only the mean size is known: each is taken to end in
@@ -405,7 +470,7 @@ inline bool few_rows(int32_t n, int32_t G, int32_t h_in, int32_t h_out, bool mx)
   const double met = std::min(n, G), weights = 1e-6 * h_in * h_out;
   const auto tiles = [&](double B) { return G == 1 ? std::ceil(n / B) : std::max(met, n / B + met / 2); };
   const bool small = n <= 16 * met;
-  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.23 : 0.38) : (small ? 0.38 : 0.5));
+  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.17 : 0.26) : (small ? 0.38 : 0.5));
   const double tiles128 = tiles(128) * std::ceil(h_out / 128.0), steps = h_in / 64.0;
   const double tiled = mx ? 0.8 * steps * std::max(1.0, tiles128 / 320)
                           : std::max(0.56 * steps * std::max(1.0, tiles128 / 512), met * weights * 2 / 4.3);
