@@ -107,7 +107,7 @@ struct Tile {
   // [fragment] of the columns
   static constexpr int SC = M == kMxBoth ? 8 * BR : 0;  // where the columns' start
   struct MxScales {
-    uint8_t b[M == kMxBoth ? 8 * (BR + BC) : M == kMxW ? 2 * BC : 16];
+    alignas(16) uint8_t b[M == kMxBoth ? 8 * (BR + BC) : M == kMxW ? 2 * BC : 16];
   };
   // LDS buffers.  kForward's 256 x 256 tile has room for a third one of the column operand: the
   // weight comes from HBM, the rows from the L2, so it is fetched two stages ahead.
@@ -377,15 +377,15 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
     uint32_t rs[NR / 2], cs[NC / 2];
     if constexpr (M == kMxW) {
       u32x2_t codes[NC];
-      const uint8_t* from = sb.b + (((kq >> 1) * WC + wc) * 16 + l16) * NC;
+      static_assert(NC == 4, "a lane's scales are one word");
+      const uint32_t scales = reinterpret_cast<const uint32_t*>(sb.b)[((kq >> 1) * WC + wc) * 16 + l16];
 #pragma unroll
       for (int j = 0; j < NC; ++j)
         codes[j] = reinterpret_cast<const u32x2_t*>(cb.v)[co[0] + 64 * j];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const uint32_t b = from[j];
-        const float f = mx_scale(b);
-        if constexpr (DT == SGMV_F16 && !SPLIT) held &= f16_holds(b, codes[j].x | codes[j].y);
+        const float f = mx_scale_at(scales, j);
+        if constexpr (DT == SGMV_F16 && !SPLIT) held &= f16_holds(scales >> (8 * j) & 255u, codes[j].x | codes[j].y);
         cv[0][j] = mx_eight<WT>(codes[j].x, f);
         cv[1][j] = mx_eight<WT>(codes[j].y, f);
       }
