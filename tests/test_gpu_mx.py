@@ -229,6 +229,28 @@ def test_enough_work_for_half_of_the_largest_tiles(torch, dtype, E, K):
         close(f64(y[part]), ref, mag, K, dtype, f"rows {lo}..")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [20, 150])
+@pytest.mark.parametrize("K", [8192, 8224, 8416])
+def test_few_rows_of_long_weights(torch, dtype, rows, K):
+    """Decode batches over enough long rows that a wavefront makes several rounds, with scales of
+    a row that start at any byte; x in 16 and in 4 bits."""
+    import adapter_gemv_amd as sgmv
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(24)
+    E, N = 8, 1064
+    x = torch.randn(rows, K, generator=gen, device="cuda").to(_dt(torch, dtype))
+    q = weights(torch, gen, E, N, K, dtype)
+    ids = torch.randint(-1, E, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    groups = sgmv.group_rows(ids, E)
+    Wd = G.mx_decode(q.codes.cpu().numpy(), q.scales.cpu().numpy())
+    for both in (False, True):
+        y = sgmv.mx_matmul(torch.full((rows, N), float("nan"), dtype=x.dtype, device="cuda"),
+                           sgmv.mx_quantize(x) if both else x, q, groups)
+        ref, mag = G.group_matmul(G.mx_decode(*G.mx_encode(f64(x))) if both else f64(x), Wd, ids.cpu().numpy())
+        close(f64(y), ref, mag, K, dtype, f"both {both}")
+
+
 @pytest.mark.parametrize("rows", [3, 40, 200, 3000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("low", [1, 60, 118, 140])
