@@ -126,7 +126,7 @@ inline int32_t shared_rows(int32_t n, int32_t share) { return (n + share - 1) / 
 
 // at most this many row tiles of BM rows in the groups and behind them
 inline int64_t max_row_tiles(int32_t n, int32_t G, bool grouped, int BM) {
-  const int64_t most = n / BM + (grouped ? G + 1 : 1);
+  const int64_t most = n / BM + (grouped ? G + 1 : n % BM != 0);
   return most < n ? most : n;
 }
 

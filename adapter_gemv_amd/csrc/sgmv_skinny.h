@@ -434,9 +434,9 @@ __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyAr
 // 4096 x 1024, 32 rows: 38 us; 40 with 8 wavefronts, 44 with 32 columns).
 // 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
 // (8 experts of 5120 x 13824, 32 rows, in the first form: 93 us; 104 with 4 wavefronts, 124 with 16
-// columns; the call is now at 89), or
-// 16 columns and 8 wavefronts where that leaves CUs without work (5120 x 13824, 16 rows: 33 and
-// 41 us; 4096 x 4096: 9.1 and 8.9).
+// columns; the call is now at 89), or 16 columns and 8 wavefronts where that leaves CUs without work
+// (now, the first and the second: 4096 x 4096, 32 rows, 17.5 and 12.1 us; 64 rows 17.9 and 22.2;
+// 4096 x 8192, 32 rows, 17.7 and 22.1; 5120 x 13824, 16 rows, 18.7 and 37.5).
 template <int DT, bool MX, bool XM, int CT, int WAVES>
 hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A, int64_t row_tiles) {
   const int64_t grid = row_tiles * ((A.h_out + 16 * CT - 1) / (16 * CT));
