@@ -154,6 +154,12 @@ extern "C" int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n
   if (n < 0 || n > kMaxGroupRows || n_groups < 1) return SGMV_ERR_SHAPE;
   if (n_groups > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
   if (!starts || (n > 0 && (!ids || !perm))) return SGMV_ERR_NULL;
+  const size_t row_bytes = sizeof(int32_t) * static_cast<size_t>(n);
+  const size_t starts_bytes = sizeof(int32_t) * (static_cast<size_t>(n_groups) + 1);
+  if (n > 0 && (ranges_overlap(perm, row_bytes, ids, row_bytes) ||
+                ranges_overlap(starts, starts_bytes, ids, row_bytes) ||
+                ranges_overlap(starts, starts_bytes, perm, row_bytes)))
+    return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
   const int grid = std::min(kGroupMost, std::max(1, n / kGroupRun));
   group_rows_kernel<<<grid, 64 * group_waves(n_groups), 0, stream>>>(ids, n, n_groups, perm, starts);

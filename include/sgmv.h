@@ -461,7 +461,8 @@ int sgmv_lora_add_host_ids_noalloc(hipStream_t stream, int32_t dtype, void* y, i
  *   perm    device int32[n] out
  *   starts  device int32[n_groups + 1] out; starts[0] = 0, starts[n_groups] = the number
  *           of rows that belong to a group
- * 1 <= n_groups <= SGMV_MAX_GROUPS.  n == 0 still writes starts (zeros).
+ * 1 <= n_groups <= SGMV_MAX_GROUPS.  n == 0 still writes starts (zeros).  ids, perm and
+ * starts must not overlap (SGMV_ERR_ALIAS).
  */
 int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n, int32_t n_groups,
                     int32_t* perm, int32_t* starts);
