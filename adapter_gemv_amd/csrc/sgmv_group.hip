@@ -179,7 +179,8 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
   if (!y || !x || !W) return SGMV_ERR_NULL;
   if (!aligned16(y) || !aligned16(x) || !aligned16(W)) return SGMV_ERR_ALIGNMENT;
   const size_t y_bytes = matrix_bytes(n, ld_y, h_out);
-  if (ranges_overlap(y, y_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
+  if (over_tables(y, y_bytes, starts, perm, n, n_groups) ||
+      ranges_overlap(y, y_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
       ranges_overlap(y, y_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
   if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
@@ -218,7 +219,8 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
   if (!dx || !dy || !W) return SGMV_ERR_NULL;
   if (!aligned16(dx) || !aligned16(dy) || !aligned16(W)) return SGMV_ERR_ALIGNMENT;
   const size_t dx_bytes = matrix_bytes(n, ld_dx, h_in);
-  if (ranges_overlap(dx, dx_bytes, dy, matrix_bytes(n, ld_dy, h_out)) ||
+  if (over_tables(dx, dx_bytes, starts, perm, n, n_groups) ||
+      ranges_overlap(dx, dx_bytes, dy, matrix_bytes(n, ld_dy, h_out)) ||
       ranges_overlap(dx, dx_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
   if (!tiles_fit(n, n_groups, starts, h_in)) return SGMV_ERR_SHAPE;
@@ -245,8 +247,9 @@ extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW,
   if (!dW || (n > 0 && (!x || !dy))) return SGMV_ERR_NULL;
   if (!aligned16(dW) || (n > 0 && (!aligned16(x) || !aligned16(dy)))) return SGMV_ERR_ALIGNMENT;
   const size_t dw_bytes = pool_bytes16(n_groups, dW_stride, int64_t(h_in) * h_out);
-  if (n > 0 && (ranges_overlap(dW, dw_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
-                ranges_overlap(dW, dw_bytes, dy, matrix_bytes(n, ld_dy, h_out))))
+  if (over_tables(dW, dw_bytes, starts, perm, n, n_groups) ||
+      (n > 0 && (ranges_overlap(dW, dw_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
+                 ranges_overlap(dW, dw_bytes, dy, matrix_bytes(n, ld_dy, h_out)))))
     return SGMV_ERR_ALIAS;
   if (static_cast<int64_t>(n_groups) * (h_out / 64 + 8) * (h_in / 64 + 8) > INT32_MAX)
     return SGMV_ERR_SHAPE;

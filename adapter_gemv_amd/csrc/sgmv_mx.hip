@@ -192,7 +192,8 @@ inline int check_mx_product(int32_t dtype, const void* y, int64_t ld_y, int32_t 
   if (!y || !W_codes || !W_scales) return SGMV_ERR_NULL;
   if (!aligned16(y) || !aligned16(W_codes) || !aligned8(W_scales)) return SGMV_ERR_ALIGNMENT;
   const size_t y_bytes = matrix_bytes(n, ld_y, h_out), elems = static_cast<size_t>(G) * h_in * h_out;
-  if (ranges_overlap(y, y_bytes, W_codes, elems / 2) || ranges_overlap(y, y_bytes, W_scales, elems / 32))
+  if (over_tables(y, y_bytes, starts, perm, n, G) || ranges_overlap(y, y_bytes, W_codes, elems / 2) ||
+      ranges_overlap(y, y_bytes, W_scales, elems / 32))
     return SGMV_ERR_ALIAS;
   return tiles_fit(n, G, starts, h_out) ? SGMV_OK : SGMV_ERR_SHAPE;
 }

@@ -121,6 +121,13 @@ inline int check_groups(int32_t n, int32_t G, int32_t share, const int32_t* star
   return SGMV_OK;
 }
 
+// whether an output lies over the tables of its call (rows are looked up until the last is written)
+inline bool over_tables(const void* out, size_t bytes, const int32_t* starts, const int32_t* perm,
+                        int32_t n, int32_t G) {
+  return (starts && ranges_overlap(out, bytes, starts, sizeof(int32_t) * (static_cast<size_t>(G) + 1))) ||
+         (perm && ranges_overlap(out, bytes, perm, sizeof(int32_t) * static_cast<size_t>(n)));
+}
+
 // rows of x that n rows sharing it read
 inline int32_t shared_rows(int32_t n, int32_t share) { return (n + share - 1) / share; }
 

@@ -449,7 +449,7 @@ int sgmv_lora_add_host_ids_noalloc(hipStream_t stream, int32_t dtype, void* y, i
  * These calls need no workspace.  Their errors are those of the other calls: SGMV_ERR_SHAPE
  * (also for n > 2^30, share < 1, n * share >= 2^31 and products of more than 2^31 - 1 tiles), SGMV_ERR_ALIGNMENT,
  * SGMV_ERR_NULL, SGMV_ERR_UNSUPPORTED (dtype; n_groups above SGMV_MAX_GROUPS),
- * SGMV_ERR_ALIAS (an output overlaps an input), SGMV_ERR_HIP.
+ * SGMV_ERR_ALIAS (an output overlaps an input, the tables among them), SGMV_ERR_HIP.
  */
 #define SGMV_MAX_GROUPS 1024
 

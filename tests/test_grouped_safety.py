@@ -16,3 +16,31 @@ def test_group_rows_outputs_stand_alone(n):
                          (PERM, IDS), (PERM, IDS + 4 * n - 4), (PERM, IDS - 4 * 7), (PERM, PERM),
                          (PERM, PERM + 4 * n - 4), (PERM, PERM - 4 * 7)):
         assert rows(None, IDS, n, 7, perm, starts) == _lib.ERR_ALIAS
+
+
+X, Y, W, SX, SW = 4 << 40, 5 << 40, 6 << 40, 7 << 40, 8 << 40
+N, G, H_IN, H_OUT = 64, 4, 256, 512
+TAIL = dict(starts=STARTS, perm=PERM, n=N, n_groups=G, h_in=H_IN, h_out=H_OUT)
+# name, arguments, the output's name and bytes
+PRODUCTS = [
+    ("sgmv_group_matmul", dict(stream=None, dtype=1, y=Y, ld_y=H_OUT, x=X, ld_x=H_IN, share=1, W=W,
+                               W_stride=H_IN * H_OUT, **TAIL), "y", 2 * N * H_OUT),
+    ("sgmv_group_matmul_dx", dict(stream=None, dtype=1, dx=Y, ld_dx=H_IN, dy=X, ld_dy=H_OUT, W=W,
+                                  W_stride=H_IN * H_OUT, **TAIL), "dx", 2 * N * H_IN),
+    ("sgmv_group_matmul_dw", dict(stream=None, dtype=1, dW=W, dW_stride=H_IN * H_OUT, x=X, ld_x=H_IN,
+                                  share=1, dy=Y, ld_dy=H_OUT, **TAIL), "dW", 2 * G * H_IN * H_OUT),
+    ("sgmv_mx_matmul", dict(stream=None, dtype=1, y=Y, ld_y=H_OUT, x=X, ld_x=H_IN, share=1, W=W,
+                            W_scales=SW, **TAIL), "y", 2 * N * H_OUT),
+    ("sgmv_mx_matmul_quantized", dict(stream=None, dtype=1, y=Y, ld_y=H_OUT, x=X, x_scales=SX, share=1,
+                                      W=W, W_scales=SW, **TAIL), "y", 2 * N * H_OUT),
+]
+
+
+@pytest.mark.parametrize("name,args,out,size", PRODUCTS, ids=[p[0] for p in PRODUCTS])
+def test_products_do_not_write_over_their_tables(name, args, out, size):
+    """Rows are looked up in the tables until the last of them is written."""
+    call = getattr(_lib.lib(), name)
+    at = args[out]
+    for kw in (dict(perm=at), dict(perm=at + size - 4), dict(perm=at - 4 * N + 4),
+               dict(starts=at + 64), dict(starts=at + size - 4), dict(starts=at - 4 * G)):
+        assert call(*{**args, **kw}.values()) == _lib.ERR_ALIAS, kw
