@@ -84,10 +84,13 @@ def _tables(groups: Optional[RowGroups], n: int, like):
         return None, None, 1
     if groups.n != n:
         raise ValueError(f"{n} rows, but the groups were made of {groups.n}")
-    if groups.table.get_device() != like.get_device():
+    table, E = groups.table, groups.n_groups
+    if table.dtype is not _torch().int32 or table.shape != (E + 1 + n,) or not table.is_contiguous():
+        raise ValueError(f"groups must hold a dense int32 table [{E + 1 + n}], as group_rows makes it")
+    if table.get_device() != like.get_device():
         raise ValueError("groups must be on the tensors' GPU")
-    at = groups.table.data_ptr()
-    return at, at + 4 * (groups.n_groups + 1), groups.n_groups
+    at = table.data_ptr()
+    return at, at + 4 * (E + 1), E
 
 
 def _share(n: int, x_rows: int) -> int:
@@ -111,10 +114,10 @@ def _pool(W, groups: Optional[RowGroups], name: str):
     return h_out, h_in, (W.stride(0) if E > 1 else h_out * h_in)
 
 
-def _same_type(*tensors):
-    if any(t.dtype != tensors[0].dtype for t in tensors):
+def _same_type(a, b, c):
+    if b.dtype != a.dtype or c.dtype != a.dtype:
         raise TypeError("all operands must share a dtype")
-    return dtype_code(tensors[0])
+    return dtype_code(a)
 
 
 def group_matmul(y, x, W, groups: Optional[RowGroups] = None, stream=None):
@@ -128,8 +131,8 @@ def group_matmul(y, x, W, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"x [., {x.shape[1]}] / y [., {y.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt, share = _same_type(y, x, W), _share(n, int(x.shape[0]))
-    handle = _stream_of(stream, y, x, W)
     starts, perm, E = _tables(groups, n, y)
+    handle = _stream_of(stream, y, x, W)
     st = _lib.lib().sgmv_group_matmul(handle, dt, y.data_ptr(), y.stride(0),
                                       x.data_ptr(), x.stride(0), share, W.data_ptr(), stride,
                                       starts, perm, n, E, h_in, h_out)
@@ -148,8 +151,8 @@ def group_matmul_dx(dx, dy, W, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"dx [., {dx.shape[1]}] / dy [., {dy.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt = _same_type(dx, dy, W)
-    handle = _stream_of(stream, dx, dy, W)
     starts, perm, E = _tables(groups, n, dx)
+    handle = _stream_of(stream, dx, dy, W)
     st = _lib.lib().sgmv_group_matmul_dx(handle, dt, dx.data_ptr(), dx.stride(0),
                                          dy.data_ptr(), dy.stride(0), W.data_ptr(), stride,
                                          starts, perm, n, E, h_in, h_out)
@@ -168,8 +171,8 @@ def group_matmul_dw(dW, x, dy, groups: Optional[RowGroups] = None, stream=None):
         raise ValueError(f"x [., {x.shape[1]}] / dy [., {dy.shape[1]}] do not match dW's "
                          f"h_in = {h_in}, h_out = {h_out}")
     dt, share = _same_type(dW, x, dy), _share(n, int(x.shape[0]))
-    handle = _stream_of(stream, dW, x, dy)
     starts, perm, E = _tables(groups, n, dW)
+    handle = _stream_of(stream, dW, x, dy)
     st = _lib.lib().sgmv_group_matmul_dw(handle, dt, dW.data_ptr(), stride,
                                          x.data_ptr(), x.stride(0), share, dy.data_ptr(),
                                          dy.stride(0), starts, perm, n, E, h_in, h_out)

@@ -107,8 +107,8 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
                          f"h_out = {h_out}")
     dt, share = dtype_code(y), _share(n, xs[0])
     if isinstance(x, MxTensor):
-        handle = _stream_of(stream, y, x.codes, x.scales, W.codes, W.scales)
         starts, perm, E = _tables(groups, n, y)
+        handle = _stream_of(stream, y, x.codes, x.scales, W.codes, W.scales)
         st = _lib.lib().sgmv_mx_matmul_quantized(
             handle, dt, y.data_ptr(), y.stride(0), x.codes.data_ptr(), x.scales.data_ptr(), share,
             W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
@@ -117,8 +117,8 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
     _check_rows(x, xs[0], "x")
     if x.dtype != y.dtype:
         raise TypeError("x and y must share a dtype")
-    handle = _stream_of(stream, y, x, W.codes, W.scales)
     starts, perm, E = _tables(groups, n, y)
+    handle = _stream_of(stream, y, x, W.codes, W.scales)
     st = _lib.lib().sgmv_mx_matmul(
         handle, dt, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0), share, W.codes.data_ptr(),
         W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)

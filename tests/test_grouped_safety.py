@@ -44,3 +44,20 @@ def test_products_do_not_write_over_their_tables(name, args, out, size):
     for kw in (dict(perm=at), dict(perm=at + size - 4), dict(perm=at - 4 * N + 4),
                dict(starts=at + 64), dict(starts=at + size - 4), dict(starts=at - 4 * G)):
         assert call(*{**args, **kw}.values()) == _lib.ERR_ALIAS, kw
+
+
+def test_products_do_not_read_past_a_table():
+    """RowGroups is public: a table that is too short, of other integers or with gaps."""
+    import torch
+    from adapter_gemv_amd import grouped, mx
+    i32, bf, u8 = torch.int32, torch.bfloat16, torch.uint8
+    x, y, w = torch.zeros(12, 64, dtype=bf), torch.zeros(12, 32, dtype=bf), torch.zeros(3, 32, 64, dtype=bf)
+    q = mx.MxTensor(torch.zeros(3, 32, 32, dtype=u8), torch.zeros(3, 32, 2, dtype=u8))
+    for table in (torch.zeros(15, dtype=i32), torch.zeros(17, dtype=i32), torch.zeros(16, dtype=torch.int64),
+                  torch.zeros(16), torch.zeros(32, dtype=i32)[::2], torch.zeros(16, 1, dtype=i32),
+                  torch.zeros(0, dtype=i32)):
+        g = grouped.RowGroups(12, 3, table)
+        for call in (lambda: grouped.group_matmul(y, x, w, g), lambda: grouped.group_matmul_dx(x, y, w, g),
+                     lambda: grouped.group_matmul_dw(w, x, y, g), lambda: mx.mx_matmul(y, x, q, g)):
+            with pytest.raises(ValueError, match="groups"):
+                call()
