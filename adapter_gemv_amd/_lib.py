@@ -142,3 +142,9 @@ def status_string(status: int) -> str:
 def check(status: int, where: str) -> None:
     if status != OK:
         raise SgmvError(status, where)
+
+
+def check_sizes(where: str, *sizes: int) -> None:
+    """Refuse sizes that the C calls' 32-bit integers do not hold (ctypes would cut them)."""
+    if max(sizes) > 0x7FFFFFFF:
+        check(ERR_SHAPE, where)

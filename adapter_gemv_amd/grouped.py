@@ -20,7 +20,7 @@ import dataclasses
 from typing import Optional
 
 from . import _lib
-from ._lib import check
+from ._lib import check, check_sizes
 from .sgmv import _check_rows, _torch, dtype_code
 
 
@@ -67,6 +67,9 @@ def group_rows(ids, n_groups: int, stream=None) -> RowGroups:
         raise ValueError("ids must be a device int32 tensor [n]")
     handle = _stream_of(stream, ids)
     n = ids.shape[0]
+    check_sizes("sgmv_group_rows", n)
+    if not 1 <= n_groups <= _lib.MAX_GROUPS:
+        check(_lib.ERR_SHAPE if n_groups < 1 else _lib.ERR_UNSUPPORTED, "sgmv_group_rows")
     if stream is None:
         table = ids.new_empty(n + n_groups + 1)
     else:
@@ -130,6 +133,7 @@ def group_matmul(y, x, W, groups: Optional[RowGroups] = None, stream=None):
     if x.shape[1] != h_in or y.shape[1] != h_out:
         raise ValueError(f"x [., {x.shape[1]}] / y [., {y.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
+    check_sizes("sgmv_group_matmul", n, h_in, h_out)
     dt, share = _same_type(y, x, W), _share(n, int(x.shape[0]))
     starts, perm, E = _tables(groups, n, y)
     handle = _stream_of(stream, y, x, W)
@@ -150,6 +154,7 @@ def group_matmul_dx(dx, dy, W, groups: Optional[RowGroups] = None, stream=None):
     if dx.shape[1] != h_in or dy.shape[1] != h_out:
         raise ValueError(f"dx [., {dx.shape[1]}] / dy [., {dy.shape[1]}] do not match W's "
                          f"h_in = {h_in}, h_out = {h_out}")
+    check_sizes("sgmv_group_matmul_dx", n, h_in, h_out)
     dt = _same_type(dx, dy, W)
     starts, perm, E = _tables(groups, n, dx)
     handle = _stream_of(stream, dx, dy, W)
@@ -170,6 +175,7 @@ def group_matmul_dw(dW, x, dy, groups: Optional[RowGroups] = None, stream=None):
     if x.shape[1] != h_in or dy.shape[1] != h_out:
         raise ValueError(f"x [., {x.shape[1]}] / dy [., {dy.shape[1]}] do not match dW's "
                          f"h_in = {h_in}, h_out = {h_out}")
+    check_sizes("sgmv_group_matmul_dw", n, h_in, h_out)
     dt, share = _same_type(dW, x, dy), _share(n, int(x.shape[0]))
     starts, perm, E = _tables(groups, n, dW)
     handle = _stream_of(stream, dW, x, dy)

@@ -13,7 +13,7 @@ import dataclasses
 from typing import Optional
 
 from . import _lib
-from ._lib import check
+from ._lib import check, check_sizes
 from .grouped import RowGroups, _on, _share, _stream_of, _tables
 from .sgmv import _check_rows, _torch, dtype_code
 
@@ -65,6 +65,7 @@ def mx_quantize(x, stream=None) -> MxTensor:
     rows, h, ld = _as_rows(x, "x")
     if h % BLOCK != 0:
         raise ValueError(f"h = {h} must be a multiple of {BLOCK}")
+    check_sizes("sgmv_mx_quantize", h)
     dt = dtype_code(x)
     handle = _stream_of(stream, x)
     lead = tuple(x.shape)[:-1]
@@ -82,6 +83,7 @@ def mx_dequantize(y, q: MxTensor, stream=None):
     if tuple(y.shape) != tuple(q.shape):
         raise ValueError(f"y {tuple(y.shape)} does not match the values' {tuple(q.shape)}")
     rows, h, ld = _as_rows(y, "y")
+    check_sizes("sgmv_mx_dequantize", h)
     dt = dtype_code(y)
     handle = _stream_of(stream, y, q.codes, q.scales)
     st = _lib.lib().sgmv_mx_dequantize(handle, dt, y.data_ptr(), ld,
@@ -105,6 +107,7 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
     if len(xs) != 2 or xs[1] != h_in or y.shape[1] != h_out:
         raise ValueError(f"x {xs} / y {tuple(y.shape)} do not match W's h_in = {h_in}, "
                          f"h_out = {h_out}")
+    check_sizes("sgmv_mx_matmul", n, h_in, h_out)
     dt, share = dtype_code(y), _share(n, xs[0])
     if isinstance(x, MxTensor):
         starts, perm, E = _tables(groups, n, y)

@@ -61,3 +61,67 @@ def test_products_do_not_read_past_a_table():
                      lambda: grouped.group_matmul_dw(w, x, y, g), lambda: mx.mx_matmul(y, x, q, g)):
             with pytest.raises(ValueError, match="groups"):
                 call()
+
+
+def recorded(monkeypatch):
+    """The bindings with their C calls written down instead of made (tensors may be of any device)."""
+    from adapter_gemv_amd import grouped, mx
+    calls = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+
+    recorder = Recorder()
+    monkeypatch.setattr(_lib, "lib", lambda: recorder)
+    monkeypatch.setattr(_lib, "status_string", lambda status: str(status))
+    for module in (grouped, mx):
+        monkeypatch.setattr(module, "_stream_of", lambda stream, *tensors: 0)
+    return grouped, mx, calls
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Sizes travel as 32-bit integers: 2^32 + 16 rows are not 16."""
+    import torch
+    grouped, mx, calls = recorded(monkeypatch)
+    bf, u8, far = torch.bfloat16, torch.uint8, (1 << 32) + 32
+
+    def empty(*shape, dtype=bf):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    x, w, q = empty(far, 32), empty(32, 32), mx.MxTensor(empty(32, 16, dtype=u8), empty(32, 1, dtype=u8))
+    wide, tall = empty(32, far), empty(far, 32)
+    ids = torch.empty(4, dtype=torch.int32)
+    for call in (lambda: grouped.group_matmul(x, x, w), lambda: grouped.group_matmul_dx(x, x, w),
+                 lambda: grouped.group_matmul_dw(w, x, x),
+                 lambda: grouped.group_matmul(empty(4, 32), empty(4, far), wide),
+                 lambda: grouped.group_matmul(empty(4, far), empty(4, 32), tall),
+                 lambda: grouped.group_matmul_dx(empty(4, far), empty(4, 32), wide),
+                 lambda: grouped.group_matmul_dw(tall, empty(4, 32), empty(4, far)),
+                 lambda: grouped.group_rows(empty(far, dtype=torch.int32), 3),
+                 lambda: grouped.group_rows(ids, (1 << 32) + 3), lambda: grouped.group_rows(ids, 1 << 32),
+                 lambda: mx.mx_matmul(x, x, q), lambda: mx.mx_matmul(x, mx.MxTensor(
+                     empty(far, 16, dtype=u8), empty(far, 1, dtype=u8)), q),
+                 lambda: mx.mx_matmul(empty(4, 32), empty(4, far), mx.MxTensor(
+                     empty(32, far // 2, dtype=u8), empty(32, far // 32, dtype=u8))),
+                 lambda: mx.mx_matmul(empty(4, far), empty(4, 32), mx.MxTensor(
+                     empty(far, 16, dtype=u8), empty(far, 1, dtype=u8))),
+                 lambda: mx.mx_quantize(empty(far)), lambda: mx.mx_quantize(wide),
+                 lambda: mx.mx_dequantize(empty(far), mx.MxTensor(empty(far // 2, dtype=u8),
+                                                                  empty(far // 32, dtype=u8)))):
+        with pytest.raises(_lib.SgmvError):
+            call()
+    assert not calls
+    # as many rows of a matrix as there are: 64-bit
+    mx.mx_quantize(tall)
+    assert calls[0][1][-2:] == (far, 32)
+
+
+@pytest.mark.parametrize("n_groups,status", [(-7, _lib.ERR_SHAPE), (0, _lib.ERR_SHAPE),
+                                             (1025, _lib.ERR_UNSUPPORTED), (1 << 40, _lib.ERR_UNSUPPORTED)])
+def test_group_rows_refuses_before_it_allocates(monkeypatch, n_groups, status):
+    import torch
+    grouped, _, calls = recorded(monkeypatch)
+    with pytest.raises(_lib.SgmvError) as refused:
+        grouped.group_rows(torch.empty(4, dtype=torch.int32), n_groups)
+    assert refused.value.status == status and not calls
