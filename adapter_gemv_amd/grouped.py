@@ -104,6 +104,11 @@ def _share(n: int, x_rows: int) -> int:
     return max(n // x_rows, 1)
 
 
+def _ld(t) -> int:
+    """Elements between the rows of a matrix; one row may have any stride."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _pool(W, groups: Optional[RowGroups], name: str):
     """A weight [E, h_out, h_in] (or [h_out, h_in] without groups): (h_out, h_in, stride)."""
     E = 1 if groups is None else groups.n_groups
@@ -137,8 +142,8 @@ def group_matmul(y, x, W, groups: Optional[RowGroups] = None, stream=None):
     dt, share = _same_type(y, x, W), _share(n, int(x.shape[0]))
     starts, perm, E = _tables(groups, n, y)
     handle = _stream_of(stream, y, x, W)
-    st = _lib.lib().sgmv_group_matmul(handle, dt, y.data_ptr(), y.stride(0),
-                                      x.data_ptr(), x.stride(0), share, W.data_ptr(), stride,
+    st = _lib.lib().sgmv_group_matmul(handle, dt, y.data_ptr(), _ld(y),
+                                      x.data_ptr(), _ld(x), share, W.data_ptr(), stride,
                                       starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul")
     return y
@@ -158,8 +163,8 @@ def group_matmul_dx(dx, dy, W, groups: Optional[RowGroups] = None, stream=None):
     dt = _same_type(dx, dy, W)
     starts, perm, E = _tables(groups, n, dx)
     handle = _stream_of(stream, dx, dy, W)
-    st = _lib.lib().sgmv_group_matmul_dx(handle, dt, dx.data_ptr(), dx.stride(0),
-                                         dy.data_ptr(), dy.stride(0), W.data_ptr(), stride,
+    st = _lib.lib().sgmv_group_matmul_dx(handle, dt, dx.data_ptr(), _ld(dx),
+                                         dy.data_ptr(), _ld(dy), W.data_ptr(), stride,
                                          starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul_dx")
     return dx
@@ -180,7 +185,7 @@ def group_matmul_dw(dW, x, dy, groups: Optional[RowGroups] = None, stream=None):
     starts, perm, E = _tables(groups, n, dW)
     handle = _stream_of(stream, dW, x, dy)
     st = _lib.lib().sgmv_group_matmul_dw(handle, dt, dW.data_ptr(), stride,
-                                         x.data_ptr(), x.stride(0), share, dy.data_ptr(),
-                                         dy.stride(0), starts, perm, n, E, h_in, h_out)
+                                         x.data_ptr(), _ld(x), share, dy.data_ptr(),
+                                         _ld(dy), starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_group_matmul_dw")
     return dW

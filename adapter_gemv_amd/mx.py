@@ -14,7 +14,7 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check, check_sizes
-from .grouped import RowGroups, _on, _share, _stream_of, _tables
+from .grouped import RowGroups, _ld, _on, _share, _stream_of, _tables
 from .sgmv import _check_rows, _torch, dtype_code
 
 BLOCK = 32
@@ -99,7 +99,9 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
     n = y.shape[0]
     _check_rows(y, n, "y")
     E = 1 if groups is None else groups.n_groups
-    shape = W.shape if len(W.shape) == 3 else (1, *W.shape)
+    shape = W.shape
+    if len(shape) == 2:
+        shape = (1, *shape)
     if len(shape) != 3 or shape[0] != E:
         raise ValueError(f"W must be [{E}, h_out, h_in]")
     _, h_out, h_in = shape
@@ -113,7 +115,7 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
         starts, perm, E = _tables(groups, n, y)
         handle = _stream_of(stream, y, x.codes, x.scales, W.codes, W.scales)
         st = _lib.lib().sgmv_mx_matmul_quantized(
-            handle, dt, y.data_ptr(), y.stride(0), x.codes.data_ptr(), x.scales.data_ptr(), share,
+            handle, dt, y.data_ptr(), _ld(y), x.codes.data_ptr(), x.scales.data_ptr(), share,
             W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
         check(st, "sgmv_mx_matmul_quantized")
         return y
@@ -123,7 +125,7 @@ def mx_matmul(y, x, W: MxTensor, groups: Optional[RowGroups] = None, stream=None
     starts, perm, E = _tables(groups, n, y)
     handle = _stream_of(stream, y, x, W.codes, W.scales)
     st = _lib.lib().sgmv_mx_matmul(
-        handle, dt, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0), share, W.codes.data_ptr(),
+        handle, dt, y.data_ptr(), _ld(y), x.data_ptr(), _ld(x), share, W.codes.data_ptr(),
         W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
     check(st, "sgmv_mx_matmul")
     return y

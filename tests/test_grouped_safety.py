@@ -125,3 +125,29 @@ def test_group_rows_refuses_before_it_allocates(monkeypatch, n_groups, status):
     with pytest.raises(_lib.SgmvError) as refused:
         grouped.group_rows(torch.empty(4, dtype=torch.int32), n_groups)
     assert refused.value.status == status and not calls
+
+
+def test_one_row_of_any_stride(monkeypatch):
+    """The distance to a next row means nothing where there is one row: tensors whose stride there
+    is 1, or no multiple of 8, are taken as mx_quantize takes them."""
+    import torch
+    grouped, mx, calls = recorded(monkeypatch)
+    bf = torch.bfloat16
+    w = torch.zeros(64, 32, dtype=bf)
+    q = mx.MxTensor(torch.zeros(64, 16, dtype=torch.uint8), torch.zeros(64, 1, dtype=torch.uint8))
+
+    def rows(h):
+        return torch.zeros(h, 1, dtype=bf).t(), torch.zeros(5, h + 3, dtype=bf)[:1, :h], torch.zeros(0, h, dtype=bf)
+
+    for x, y in zip(rows(32), rows(64)):
+        grouped.group_matmul(y, x, w)
+        grouped.group_matmul_dx(x, y, w)
+        grouped.group_matmul_dw(w, x, y)
+        mx.mx_matmul(y, x, q)
+        mx.mx_matmul(y, mx.mx_quantize(x), q)
+    strides = dict(sgmv_group_matmul=((3, 64), (5, 32)), sgmv_group_matmul_dx=((3, 32), (5, 64)),
+                   sgmv_group_matmul_dw=((5, 32), (8, 64)), sgmv_mx_matmul=((3, 64), (5, 32)),
+                   sgmv_mx_matmul_quantized=((3, 64),), sgmv_mx_quantize=((5, 32),))
+    assert len(calls) == 3 * 6
+    for name, args in calls:
+        assert all(args[at] == ld for at, ld in strides[name]), (name, args)
