@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Optional, Sequence, Union
 
 import numpy as np
@@ -121,6 +122,7 @@ def sgmv_lora_add(stream, dtype, y, ld_y, x, ld_x, A_ptrs, B_ptrs, seg_starts, p
 # --------------------------------------------------------------------------------------
 # torch layer
 # --------------------------------------------------------------------------------------
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
