@@ -13,10 +13,13 @@
 // elements of every block, as in the 16-bit form, so that 4 lanes read 64 bytes of x side by side
 // (two whole blocks to a lane, and 16 bytes of x out of every 128 for each load: 10 % slower), and
 // the scales of four units are fetched at once and dealt out between lanes.
-// bfloat16 holds every element times its scale exactly, so the scale goes in with the
-// conversion.  float16 does for scales 2^-23 .. 2^13 (and for blocks of zeros); a workgroup
-// that meets another one starts again with x taken apart into two bfloat16 (8 + 3 of its 11
-// bits), as two exact bfloat16 products.  With x in 4 bits too, both sides are bfloat16.
+// bfloat16 holds every element times its scale exactly for scales up to 2^125, so the scale goes
+// in with the conversion.  float16 does for scales 2^-23 .. 2^13 (and for blocks of zeros); a
+// workgroup that meets another one starts again with x taken apart into two bfloat16 (8 + 3 of its
+// 11 bits), as two exact bfloat16 products.  With x in 4 bits too, both sides are bfloat16.  An
+// element past bfloat16's range becomes an infinity, and so do the sums it is part of (or NaN): a
+// workgroup with such sums looks for scales above 2^125, and computes its outputs again, another
+// way, if it has one (mx_mend).
 #pragma once
 
 #include <algorithm>
@@ -115,6 +118,90 @@ __device__ __forceinline__ void tile_for(F&& f) {
   }
 }
 
+// A product with 4-bit weights, for mx_any_scale
+struct MxProduct {
+  const RowTab& T;
+  const Share& share;
+  const uint16_t* x;         // 16-bit rows, or codes
+  const uint8_t* x_scales;
+  int64_t ld_x;              // elements (16-bit rows)
+  const char* w;
+  const uint8_t* scales;
+  int64_t w_group;           // bytes between groups of w
+  uint16_t* y;
+  int64_t ld_y;
+  int32_t h_in, h_out;
+};
+
+// Whether columns c0 .. c0 + cols - 1 of the tile's group (or the tile's rows of x) have a block
+// whose scale, 2^126 or 2^127, may take an element past bfloat16's range.  By the whole workgroup.
+template <bool XM>
+__device__ __forceinline__ bool mx_past_range(const MxProduct& P, const RowTile& t, int c0, int cols) {
+  const int blocks = P.h_in / 32;
+  bool found = false;
+  const uint8_t* const ws = P.scales + t.g * (P.w_group / 16) + static_cast<int64_t>(c0) * blocks;
+  const int64_t mine = static_cast<int64_t>(min(cols, P.h_out - c0)) * blocks;
+  for (int64_t i = threadIdx.x; i < mine; i += blockDim.x) found |= ws[i] - 253u <= 1u;
+  if constexpr (XM) {
+    for (int r = 0; r < t.rows; ++r) {
+      const uint8_t* const xs = P.x_scales + P.share.div(P.T.row(t.row0 + r)) * static_cast<int64_t>(blocks);
+      for (int b = threadIdx.x; b < blocks; b += blockDim.x) found |= xs[b] - 253u <= 1u;
+    }
+  }
+  return __syncthreads_or(found);
+}
+
+// The outputs of a row tile's columns c0 .. c0 + cols - 1 for scales of any size, by the whole
+// workgroup: an output to a thread, every block summed as if its scale were 2^-8 (no sum of 32
+// products then passes float32) and scaled after.  Slow (every operand read again and again), for
+// values past 2^127, which no weight of a model has.
+template <int DT, bool XM>
+__device__ __forceinline__ void mx_any_scale(const MxProduct& P, const RowTile& t, int c0, int cols) {
+  const int blocks = P.h_in / 32;
+  for (int i = threadIdx.x; i < t.rows * cols; i += blockDim.x) {
+    const int c = c0 + i % cols;
+    if (c >= P.h_out) continue;
+    const int row = P.T.row(t.row0 + i / cols), of = P.share.div(row);
+    const char* const w = P.w + t.g * P.w_group + static_cast<int64_t>(c) * (P.h_in / 2);
+    const uint8_t* const ws = P.scales + t.g * (P.w_group / 16) + static_cast<int64_t>(c) * blocks;
+    const uint16_t* const x = P.x + of * (XM ? static_cast<int64_t>(P.h_in) / 4 : P.ld_x);
+    float acc = 0.f;
+    for (int b = 0; b < blocks; ++b) {
+      int power = ws[b] - 127 + 8;
+      bool nan = ws[b] == 255;
+      if constexpr (XM) {
+        const uint32_t xb = P.x_scales[of * static_cast<int64_t>(blocks) + b];
+        power += static_cast<int>(xb) - 127;
+        nan |= xb == 255;
+      }
+      float sum = 0.f;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t codes = reinterpret_cast<const uint32_t*>(w)[4 * b + k];
+        const uint4 v = mx_eight<SGMV_BF16>(codes, 0x1p-8f);
+        const uint4 u = XM ? mx_eight<SGMV_BF16>(reinterpret_cast<const uint32_t*>(x)[4 * b + k], 1.f)
+                           : ld16(x + 32 * b + 8 * k);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          using X = Elem<XM ? SGMV_BF16 : DT>;
+          sum = fmaf(Elem<SGMV_BF16>::lo(word(v, h)), X::lo(word(u, h)), sum);
+          sum = fmaf(Elem<SGMV_BF16>::hi(word(v, h)), X::hi(word(u, h)), sum);
+        }
+      }
+      acc += nan ? __builtin_nanf("") : ldexpf(sum, power);
+    }
+    P.y[row * P.ld_y + c] = static_cast<uint16_t>(Elem<DT>::pack(acc, 0.f));
+  }
+}
+
+// After a workgroup wrote its outputs, `finite` telling whether each thread's sums were: where some
+// were not, because an element passed bfloat16's range, they are computed again.  The test at the
+// end costs less than a hundredth of a call; looking at every scale in the loop cost bfloat16
+// decode batches 1.5 to 3.5 hundredths.
+template <int DT, bool XM>
+__device__ __forceinline__ void mx_mend(const MxProduct& P, const RowTile& t, int c0, int cols, bool finite) {
+  if (!__syncthreads_and(finite) && mx_past_range<XM>(P, t, c0, cols)) mx_any_scale<DT, XM>(P, t, c0, cols);
+}
+
 // XM: x in 4 bits (its rows dense), DT the type of y alone
 template <int DT, bool MX, bool XM, int CT, int WAVES>
 struct Skinny {
@@ -128,7 +215,7 @@ struct Skinny {
   };
 
   // This wavefront's part of the products, in acc.  False where float16 did not hold a weight
-  // (never with SPLIT, the exact way for any scale).
+  // (never with SPLIT, the exact way for scales up to 2^125).
   template <int MT, bool SPLIT>
   static __device__ __forceinline__ bool multiply_rows(const SkinnyArgs& A, const RowTile& t, int c0,
                                                        f32x4_t (*acc)[CT], Ring& r0, Ring& r1, Ring& r2,
@@ -388,17 +475,19 @@ struct Skinny {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   }
 
+  // false: some sum is an infinity or NaN
   template <int MT>
-  static __device__ __forceinline__ void run(const SkinnyArgs& A, const RowTile& t, int c0, Ring& r0, Ring& r1,
+  static __device__ __forceinline__ bool run(const SkinnyArgs& A, const RowTile& t, int c0, Ring& r0, Ring& r1,
                                              Ring& r2, Ring& r3, float (*sums)[16][16 * CT + 4]) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, kq = lane >> 4;
+    constexpr int COLS = 16 * CT;
     f32x4_t acc[MT][CT];
     const bool held = multiply_rows<MT, false>(A, t, c0, acc, r0, r1, r2, r3);
     if constexpr (MX && CTYPE == SGMV_F16) {
       if (!__syncthreads_and(held)) multiply_rows<MT, true>(A, t, c0, acc, r0, r1, r2, r3);
     }
+    float zero = 0.f;
     // sums of the wavefronts, 16 rows at a time
-    constexpr int COLS = 16 * CT;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m) __syncthreads();
@@ -412,11 +501,13 @@ struct Skinny {
           float s = 0.f;
 #pragma unroll
           for (int v = 0; v < WAVES; ++v) s += sums[v][r][c];
+          zero = fmaf(s, 0.f, zero);
           A.y[A.T.row(t.row0 + 16 * m + r) * A.ld_y + c0 + c] =
               static_cast<uint16_t>(Elem<DT>::pack(s, 0.f));
         }
       }
     }
+    return zero == 0.f;
   }
 };
 
@@ -437,8 +528,11 @@ __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyAr
     }
     return;
   }
-  if (t.rows <= 16) S::template run<1>(A, t, c0, r0, r1, r2, r3, sums);
-  else S::template run<2>(A, t, c0, r0, r1, r2, r3, sums);
+  const bool finite = t.rows <= 16 ? S::template run<1>(A, t, c0, r0, r1, r2, r3, sums)
+                                   : S::template run<2>(A, t, c0, r0, r1, r2, r3, sums);
+  if constexpr (MX)
+    mx_mend<DT, XM>({A.T, A.share, A.x, A.x_scales, A.ld_x, A.w, A.scales, A.w_group, A.y, A.ld_y, A.h_in, A.h_out},
+                    t, c0, 16 * CT, finite);
 }
 
 // Columns and wavefronts of a workgroup.  16-bit weights: 16 columns, 4 wavefronts (64 experts of

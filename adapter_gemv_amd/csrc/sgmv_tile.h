@@ -24,9 +24,11 @@
 //
 // Weights in 4 bits against 16-bit rows (kMxW): a stage of a weight row is 32 bytes of codes
 // (kCodes); a lane reads 16 codes, one half for each half of the stage, and converts them with
-// their scale to the 16-bit operand, exactly in bfloat16.  float16 holds an element times its
-// scale for scales 2^-23 .. 2^13 (and blocks of zeros); a tile that meets another one starts
-// again in bfloat16, the rows taken apart into two bfloat16 parts (8 + 3 of their 11 bits).
+// their scale to the 16-bit operand, exactly in bfloat16 for scales up to 2^125.  float16 holds an
+// element times its scale for scales 2^-23 .. 2^13 (and blocks of zeros); a tile that meets another
+// one starts again in bfloat16, the rows taken apart into two bfloat16 parts (8 + 3 of their 11
+// bits).  A tile with infinite sums looks for scales above 2^125, and is computed again by
+// mx_any_scale if it has one, as in the streaming form.
 // Both sides in 4 bits (kMxBoth): the fragments are the 16x16x128 scaled MFMA's operands, whose
 // blocks of 32 are the format's own; the scale bytes go through LDS in the order in which its
 // byte selectors take them.
@@ -500,6 +502,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) row[i] = A.T.perm[row[i]];
   }
+  float zero = 0.f;  // kMxW: NaN once a sum is not finite
   uint16_t* const out = A.out + (DW ? static_cast<int64_t>(t.g) * A.out_group : 0);
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
@@ -515,7 +518,15 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
       const int c = c0 + (wc * NC + j + (kq & 1)) * 16 + 8 * (kq >> 1);
       const uint32_t o[4] = {lo[0], hi[0], lo[1], hi[1]};
       if (in && c < A.cols) store_words<4>(to + c, o);
+      if constexpr (M == kMxW)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) zero = fmaf(a[v], 0.f, fmaf(b[v], 0.f, zero));
     }
+  }
+  if constexpr (M == kMxW) {
+    if (nst > 0)
+      mx_mend<DT, false>({A.T, A.share, reinterpret_cast<const uint16_t*>(A.r), nullptr, A.ld_r / 2, A.c, A.c_scale,
+                          A.c_group, A.out, A.ld_out, A.depth / 2, A.cols}, t, c0, BC, zero == 0.f);
   }
 }
 

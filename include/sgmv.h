@@ -511,8 +511,9 @@ int sgmv_mx_dequantize(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
  * values of W_codes + g * h_out * h_in / 2 and W_scales + g * h_out * h_in / 32 (groups
  * dense, blocks along h_in, h_in a multiple of 32).  x is dtype, as y: the form for decode
  * batches, which stream the weight, and for prompts that keep 16-bit activations.
- * Elements and scales take part exactly (no weight is rounded on its way to the product);
- * sums are float32.
+ * Elements and scales take part exactly, whatever the scale (no weight is rounded on its way to
+ * the product); sums are float32.  Elements past bfloat16's range (bytes 253 and 254) make their
+ * output tile many times slower.
  */
 int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* x,
                    int64_t ld_x, int32_t share, const void* W_codes, const void* W_scales,
