@@ -129,24 +129,6 @@ inline int check_weights(int64_t stride, int32_t h_in, int32_t h_out) {
   return stride % 8 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
 }
 
-template <int DT, int B, int WR, int WC>
-hipError_t launch_dw(hipStream_t s, const TileArgs& A) {
-  const int64_t t = static_cast<int64_t>((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
-  const int64_t tiles = (t + kTileXcds - 1) / kTileXcds * kTileXcds * A.T.G;
-  return A.T.perm ? launch_tile<DT, kDw, B, B, WR, WC, true>(s, tiles, A)
-                  : launch_tile<DT, kDw, B, B, WR, WC, false>(s, tiles, A);
-}
-
-hipError_t launch_dw(int32_t dtype, hipStream_t s, const TileArgs& A) {
-  const bool f16 = dtype == SGMV_F16;
-  const auto tiles = [&](int B) {
-    return static_cast<double>(A.T.G) * ((A.rows + B - 1) / B) * ((A.cols + B - 1) / B);
-  };
-  if (big_tiles(tiles(256), tiles(128)))
-    return f16 ? launch_dw<SGMV_F16, 256, 2, 4>(s, A) : launch_dw<SGMV_BF16, 256, 2, 4>(s, A);
-  return f16 ? launch_dw<SGMV_F16, 128, 2, 2>(s, A) : launch_dw<SGMV_BF16, 128, 2, 2>(s, A);
-}
-
 }  // namespace
 
 extern "C" int sgmv_group_rows(hipStream_t stream, const int32_t* ids, int32_t n, int32_t n_groups,
@@ -185,7 +167,8 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
     return SGMV_ERR_ALIAS;
   if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
-  if (few_rows(n, n_groups, h_in, h_out, false)) {
+  const Launch L = rows_launch(kForward, n, n_groups, starts, h_in, h_out);
+  if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -203,7 +186,7 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
   A.out = static_cast<uint16_t*>(y);
   A.ld_r = 2 * ld_x, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_y, A.c_group = 2 * W_stride;
   A.cols = h_out, A.depth = 2 * h_in;
-  return hip_status(launch_rows<kForward>(dtype, stream, A));
+  return hip_status(launch_tiles<kForward>(dtype, stream, A, L));
 }
 
 extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
@@ -232,7 +215,7 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
   A.out = static_cast<uint16_t*>(dx);
   A.ld_r = 2 * ld_dy, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_dx, A.c_group = 2 * W_stride;
   A.cols = h_in, A.depth = h_out;
-  return hip_status(launch_rows<kDx>(dtype, stream, A));
+  return hip_status(launch_tiles<kDx>(dtype, stream, A, rows_launch(kDx, n, n_groups, starts, h_in, h_out)));
 }
 
 extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,
@@ -262,5 +245,6 @@ extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW,
   A.out = static_cast<uint16_t*>(dW);
   A.ld_r = 2 * ld_dy, A.ld_c = 2 * ld_x, A.ld_out = h_in, A.out_group = dW_stride;
   A.rows = h_out, A.cols = h_in;
-  return hip_status(launch_dw(dtype, stream, A));
+  const Launch L = dw_launch(n_groups, h_in, h_out);
+  return hip_status(perm ? launch_tiles<kDw, true>(dtype, stream, A, L) : launch_tiles<kDw, false>(dtype, stream, A, L));
 }

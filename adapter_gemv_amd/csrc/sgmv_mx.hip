@@ -213,7 +213,8 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
-  if (few_rows(n, n_groups, h_in, h_out, true)) {
+  const Launch L = rows_launch(kMxW, n, n_groups, starts, h_in, h_out);
+  if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -235,7 +236,7 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   A.ld_r = 2 * ld_x, A.ld_c = h_in / 2, A.ld_out = ld_y;
   A.c_group = static_cast<int64_t>(h_in) * h_out / 2;
   A.cols = h_out, A.depth = 2 * h_in;
-  return hip_status(launch_rows<kMxW>(dtype, stream, A));
+  return hip_status(launch_tiles<kMxW>(dtype, stream, A, L));
 }
 
 extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
@@ -253,7 +254,8 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
   if (ranges_overlap(y, y_bytes, x_codes, elems / 2) || ranges_overlap(y, y_bytes, x_scales, elems / 32))
     return SGMV_ERR_ALIAS;
   if ((st = check_device())) return st;
-  if (few_rows(n, n_groups, h_in, h_out, true)) {
+  const Launch L = rows_launch(kMxBoth, n, n_groups, starts, h_in, h_out);
+  if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
     S.share = share_of(share);
@@ -277,6 +279,6 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
   A.ld_r = h_in / 2, A.ld_c = h_in / 2, A.ld_out = ld_y;
   A.c_group = static_cast<int64_t>(h_in) * h_out / 2;
   A.cols = h_out, A.depth = h_in / 2;
-  return hip_status(h_in % 256 == 0 ? launch_rows<kMxBoth, true>(dtype, stream, A)
-                                    : launch_rows<kMxBoth, false>(dtype, stream, A));
+  return hip_status(h_in % 256 == 0 ? launch_tiles<kMxBoth, true>(dtype, stream, A, L)
+                                    : launch_tiles<kMxBoth, false>(dtype, stream, A, L));
 }

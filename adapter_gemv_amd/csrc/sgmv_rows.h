@@ -1,9 +1,9 @@
-// Group tables on the device and the host checks shared by the grouped products
-// (sgmv_group.hip) and the products with microscaled 4-bit weights (sgmv_mx.hip).
+// Group tables on the device, shared by the grouped products (sgmv_group.hip) and the products
+// with microscaled 4-bit weights (sgmv_mx.hip).
 #pragma once
 
-#include "sgmv_checks.h"
 #include "sgmv_device.h"
+#include "sgmv_rules.h"
 
 namespace sgmv_dev {
 
@@ -100,51 +100,9 @@ struct TileList {
 
 namespace sgmv_host {
 
-constexpr int kMaxGroups = SGMV_MAX_GROUPS;
-constexpr int32_t kMaxGroupRows = 1 << 30;  // row numbers plus a workgroup's stride stay int32
-
 inline sgmv_dev::Share share_of(int32_t share) {
   if (share == 1) return {0u, ~0u};
   return {static_cast<uint32_t>(((uint64_t(1) << 32) + share - 1) / static_cast<uint64_t>(share)), 0u};
-}
-
-inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
-// tables and group count of a grouped call; 0 when fine (n may be 0)
-inline int check_groups(int32_t n, int32_t G, int32_t share, const int32_t* starts,
-                        const int32_t* perm) {
-  if (n < 0 || n > kMaxGroupRows || G < 1 || share < 1) return SGMV_ERR_SHAPE;
-  if (G > kMaxGroups) return SGMV_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(n) * share > INT32_MAX) return SGMV_ERR_SHAPE;
-  if (!starts && G != 1) return SGMV_ERR_NULL;
-  if (n > 0 && (starts == nullptr) != (perm == nullptr)) return SGMV_ERR_NULL;
-  return SGMV_OK;
-}
-
-// whether an output lies over the tables of its call (rows are looked up until the last is written)
-inline bool over_tables(const void* out, size_t bytes, const int32_t* starts, const int32_t* perm,
-                        int32_t n, int32_t G) {
-  return (starts && ranges_overlap(out, bytes, starts, sizeof(int32_t) * (static_cast<size_t>(G) + 1))) ||
-         (perm && ranges_overlap(out, bytes, perm, sizeof(int32_t) * static_cast<size_t>(n)));
-}
-
-// rows of x that n rows sharing it read
-inline int32_t shared_rows(int32_t n, int32_t share) { return (n + share - 1) / share; }
-
-// at most this many row tiles of BM rows in the groups and behind them
-inline int64_t max_row_tiles(int32_t n, int32_t G, bool grouped, int BM) {
-  const int64_t most = n / BM + (grouped ? G + 1 : n % BM != 0);
-  return most < n ? most : n;
-}
-
-// whether the tiles of a product of n rows and `cols` columns can be launched, at the smallest
-// tile
-inline bool tiles_fit(int32_t n, int32_t G, bool grouped, int32_t cols) {
-  return max_row_tiles(n, G, grouped, 16) * (cols / 16 + 8) <= INT32_MAX;
-}
-
-inline size_t pool_bytes16(int32_t G, int64_t stride, int64_t elems) {
-  return 2 * (static_cast<size_t>(G - 1) * static_cast<size_t>(stride) + static_cast<size_t>(elems));
 }
 
 }  // namespace sgmv_host

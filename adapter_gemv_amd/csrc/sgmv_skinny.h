@@ -22,8 +22,6 @@
 // way, if it has one (mx_mend).
 #pragma once
 
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "sgmv_rows.h"
@@ -43,7 +41,7 @@ struct SkinnyArgs {
   int32_t h_in, h_out;
 };
 
-constexpr int kSkinnyRows = 32;
+using sgmv_host::kSkinnyRows;
 
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
@@ -535,51 +533,23 @@ __global__ __launch_bounds__(64 * WAVES, MX ? 2 : 4) void skinny_kernel(SkinnyAr
                     t, c0, 16 * CT, finite);
 }
 
-// Columns and wavefronts of a workgroup.  16-bit weights: 16 columns, 4 wavefronts (64 experts of
-// 4096 x 1024, 32 rows: 38 us; 40 with 8 wavefronts, 44 with 32 columns).
-// 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
-// (8 experts of 5120 x 13824, 32 rows, in the first form: 93 us; 104 with 4 wavefronts, 124 with 16
-// columns; the call is now at 89), or 16 columns and 8 wavefronts where that leaves CUs without work
-// (now, the first and the second: 4096 x 4096, 32 rows, 17.5 and 12.1 us; 64 rows 17.9 and 22.2;
-// 4096 x 8192, 32 rows, 17.7 and 22.1; 5120 x 13824, 16 rows, 18.7 and 37.5).
 template <int DT, bool MX, bool XM, int CT, int WAVES>
-hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A, int64_t row_tiles) {
-  const int64_t grid = row_tiles * ((A.h_out + 16 * CT - 1) / (16 * CT));
-  skinny_kernel<DT, MX, XM, CT, WAVES><<<static_cast<uint32_t>(grid), 64 * WAVES, 0, s>>>(A);
+hipError_t launch_skinny(hipStream_t s, const SkinnyArgs& A, const sgmv_host::Launch& L) {
+  skinny_kernel<DT, MX, XM, CT, WAVES><<<static_cast<uint32_t>(L.workgroups), 64 * WAVES, 0, s>>>(A);
   return hipGetLastError();
 }
 
 template <bool MX, bool XM>
 hipError_t launch_skinny(int32_t dtype, hipStream_t s, const SkinnyArgs& A) {
-  const int64_t row_tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, kSkinnyRows);
+  const sgmv_host::Launch L = sgmv_host::skinny_launch(A.T.n, A.T.G, A.T.starts, A.h_out, MX);
   const bool f16 = dtype == SGMV_F16;
   if constexpr (!MX)
-    return f16 ? launch_skinny<SGMV_F16, false, false, 1, 4>(s, A, row_tiles)
-               : launch_skinny<SGMV_BF16, false, false, 1, 4>(s, A, row_tiles);
-  else if (row_tiles * (A.h_out / 32) >= 256)
-    return f16 ? launch_skinny<SGMV_F16, true, XM, 2, 2>(s, A, row_tiles)
-               : launch_skinny<SGMV_BF16, true, XM, 2, 2>(s, A, row_tiles);
+    return f16 ? launch_skinny<SGMV_F16, false, false, 1, 4>(s, A, L)
+               : launch_skinny<SGMV_BF16, false, false, 1, 4>(s, A, L);
+  else if (L.cols == 32)
+    return f16 ? launch_skinny<SGMV_F16, true, XM, 2, 2>(s, A, L) : launch_skinny<SGMV_BF16, true, XM, 2, 2>(s, A, L);
   else
-    return f16 ? launch_skinny<SGMV_F16, true, XM, 1, 8>(s, A, row_tiles)
-               : launch_skinny<SGMV_BF16, true, XM, 1, 8>(s, A, row_tiles);
-}
-
-// Whether few rows meet each weight, so that streaming beats tiles: the smaller of two estimates,
-// in microseconds.  Both were fitted to 1 to 64 groups of 8 to 256 rows (weights 4096 x 1024 to
-// 5120 x 13824).  Streaming takes 0.38 to 0.5 us (16-bit) or 0.17 to 0.26 us (4-bit) for a million
-// weights and row tile, the less where the rows are at most 16.  Tiles of 128 x 128 take 0.56 us
-// (4-bit: 0.8 us) for 64 contracted elements and round of the card, and for 16-bit weights no less
-// than the stream at 4.3 TB/s.  Of groups only the mean size is known: each is taken to end in
-// half a tile.
-inline bool few_rows(int32_t n, int32_t G, int32_t h_in, int32_t h_out, bool mx) {
-  const double met = std::min(n, G), weights = 1e-6 * h_in * h_out;
-  const auto tiles = [&](double B) { return G == 1 ? std::ceil(n / B) : std::max(met, n / B + met / 2); };
-  const bool small = n <= 16 * met;
-  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.17 : 0.26) : (small ? 0.38 : 0.5));
-  const double tiles128 = tiles(128) * std::ceil(h_out / 128.0), steps = h_in / 64.0;
-  const double tiled = mx ? 0.8 * steps * std::max(1.0, tiles128 / 320)
-                          : std::max(0.56 * steps * std::max(1.0, tiles128 / 512), met * weights * 2 / 4.3);
-  return stream < tiled;
+    return f16 ? launch_skinny<SGMV_F16, true, XM, 1, 8>(s, A, L) : launch_skinny<SGMV_BF16, true, XM, 1, 8>(s, A, L);
 }
 
 }  // namespace sgmv_dev

@@ -42,8 +42,6 @@
 // columns past the end repeat the last one and are not stored.
 #pragma once
 
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "sgmv_skinny.h"
@@ -51,7 +49,6 @@
 namespace sgmv_dev {
 
 enum Form { kAlong, kAcross, kCodes };
-enum Mode { kForward, kDx, kDw, kMxW, kMxBoth };
 
 typedef __attribute__((ext_vector_type(8))) int i32x8_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
@@ -122,7 +119,7 @@ struct Tile {
   static constexpr int DC = M == kForward && BR == 256 ? 3 : 2;
 };
 
-constexpr int kTileXcds = 8;
+using sgmv_host::kTileXcds;
 
 // place `i` of R x C tiles taken in bands of 8 rows, columns outer within a band: the tiles
 // that run together then share few row and column operands
@@ -530,69 +527,24 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void tile_kernel(TileArgs A) {
   }
 }
 
-// Tile size.  256 x 256 (one workgroup to a CU) runs full tiles at 1.3 times the rate of
-// 128 x 128 (two to a CU; 8192^3, bfloat16: 1470 and 1150 TFLOP/s), but wastes more where groups
-// or columns end and needs four times the tiles' room to fill the card.  What counts is rounds of
-// the 256 CUs: a round of 128 x 128 tiles takes 0.64 to 0.75 of one of 256 x 256 (measured at
-// 8 groups of 256 to 1024 rows).  A group's last tile is taken to be half full.
-constexpr int kCus = 256;
-
-inline bool big_tiles(double tiles256, double tiles128) {
-  return std::ceil(tiles256 / kCus) <= 0.7 * std::ceil(tiles128 / (2 * kCus));
-}
-
-// With 4-bit weights there is room for 128 rows x 256 columns, two workgroups to a CU: half as much
-// of a group's last tile is empty, and each weight is still turned into 16 bits only once for 128
-// rows.  For 64 stages (4096 contracted elements) a CU takes 118 us for a tile of 256 x 256, 67 us
-// for one of 128 x 256 and 54 us for one of 128 x 128, whether one or two of the latter run
-// together.  Measured with each: 8 groups of 192 rows, 4096 x 8192, 126 us against 165 with
-// 128 x 128; of 256 rows, 133 against 127 with 256 x 256; 64 groups of 384 rows, 4096 x 1024, 225
-// against 257; one of 1024 rows, 4096 x 4096, 69 against 57 with 128 x 128, of 2048 rows 77
-// against 106.
-template <typename F>
-int mx_tile(F tiles) {
-  const auto time = [](double one, double n) { return one * std::ceil(n / kCus); };
-  const double big = time(1, tiles(256, 256)), half = time(0.57, tiles(128, 256)),
-               small = time(0.46, tiles(128, 128));
-  return big <= std::min(half, small) ? 0 : half < small ? 1 : 2;
-}
-
 template <int DT, Mode M, int BR, int BC, int WR, int WC, bool WHOLE = true>
-hipError_t launch_tile(hipStream_t s, int64_t tiles, const TileArgs& A) {
-  const uint32_t grid = static_cast<uint32_t>((tiles + kTileXcds - 1) / kTileXcds * kTileXcds);
-  tile_kernel<DT, M, BR, BC, WR, WC, WHOLE><<<grid, 64 * WR * WC, 0, s>>>(A);
+hipError_t launch_tile(hipStream_t s, const TileArgs& A, const sgmv_host::Launch& L) {
+  tile_kernel<DT, M, BR, BC, WR, WC, WHOLE><<<static_cast<uint32_t>(L.workgroups), 64 * WR * WC, 0, s>>>(A);
   return hipGetLastError();
 }
 
-// row tiles of every group (and of the rows of none) times column tiles
 template <Mode M, bool WHOLE = true>
-hipError_t launch_rows(int32_t dtype, hipStream_t s, const TileArgs& A) {
-  const auto columns = [&](int BC) { return (A.cols + BC - 1) / BC; };
-  const auto expected = [&](int BR, int BC) {
-    const double n = A.T.n;
-    return (A.T.starts ? n / BR + 0.5 * std::min(A.T.n, A.T.G) : std::ceil(n / BR)) * columns(BC);
-  };
+hipError_t launch_tiles(int32_t dtype, hipStream_t s, const TileArgs& A, const sgmv_host::Launch& L) {
   const bool f16 = dtype == SGMV_F16;
-  bool big = false;
-  if constexpr (M == kMxW) {
-    const int tile = mx_tile(expected);
-    big = tile == 0;
-    if (tile == 1) {
-      const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 128) * columns(256);
-      return f16 ? launch_tile<SGMV_F16, M, 128, 256, 1, 4, WHOLE>(s, tiles, A)
-                 : launch_tile<SGMV_BF16, M, 128, 256, 1, 4, WHOLE>(s, tiles, A);
-    }
-  } else {
-    big = big_tiles(expected(256, 256), expected(128, 128));
-  }
-  if (big) {
-    const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 256) * columns(256);
-    return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A)
-               : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, tiles, A);
-  }
-  const int64_t tiles = sgmv_host::max_row_tiles(A.T.n, A.T.G, A.T.starts, 128) * columns(128);
-  return f16 ? launch_tile<SGMV_F16, M, 128, 128, 2, 2, WHOLE>(s, tiles, A)
-             : launch_tile<SGMV_BF16, M, 128, 128, 2, 2, WHOLE>(s, tiles, A);
+  if constexpr (M == kMxW)
+    if (L.rows == 128 && L.cols == 256)
+      return f16 ? launch_tile<SGMV_F16, M, 128, 256, 1, 4, WHOLE>(s, A, L)
+                 : launch_tile<SGMV_BF16, M, 128, 256, 1, 4, WHOLE>(s, A, L);
+  if (L.rows == 256)
+    return f16 ? launch_tile<SGMV_F16, M, 256, 256, 2, 4, WHOLE>(s, A, L)
+               : launch_tile<SGMV_BF16, M, 256, 256, 2, 4, WHOLE>(s, A, L);
+  return f16 ? launch_tile<SGMV_F16, M, 128, 128, 2, 2, WHOLE>(s, A, L)
+             : launch_tile<SGMV_BF16, M, 128, 128, 2, 2, WHOLE>(s, A, L);
 }
 
 }  // namespace sgmv_dev
