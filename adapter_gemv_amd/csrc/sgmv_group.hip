@@ -165,9 +165,9 @@ extern "C" int sgmv_group_matmul(hipStream_t stream, int32_t dtype, void* y, int
       ranges_overlap(y, y_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
       ranges_overlap(y, y_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
-  if (!tiles_fit(n, n_groups, starts, h_out)) return SGMV_ERR_SHAPE;
-  if ((st = check_device())) return st;
   const Launch L = rows_launch(kForward, n, n_groups, starts, h_in, h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
   if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
@@ -206,7 +206,8 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
       ranges_overlap(dx, dx_bytes, dy, matrix_bytes(n, ld_dy, h_out)) ||
       ranges_overlap(dx, dx_bytes, W, pool_bytes16(n_groups, W_stride, int64_t(h_in) * h_out)))
     return SGMV_ERR_ALIAS;
-  if (!tiles_fit(n, n_groups, starts, h_in)) return SGMV_ERR_SHAPE;
+  const Launch L = rows_launch(kDx, n, n_groups, starts, h_in, h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};
@@ -215,7 +216,7 @@ extern "C" int sgmv_group_matmul_dx(hipStream_t stream, int32_t dtype, void* dx,
   A.out = static_cast<uint16_t*>(dx);
   A.ld_r = 2 * ld_dy, A.ld_c = 2 * static_cast<int64_t>(h_in), A.ld_out = ld_dx, A.c_group = 2 * W_stride;
   A.cols = h_in, A.depth = h_out;
-  return hip_status(launch_tiles<kDx>(dtype, stream, A, rows_launch(kDx, n, n_groups, starts, h_in, h_out)));
+  return hip_status(launch_tiles<kDx>(dtype, stream, A, L));
 }
 
 extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW, int64_t dW_stride,
@@ -234,8 +235,8 @@ extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW,
       (n > 0 && (ranges_overlap(dW, dw_bytes, x, matrix_bytes(shared_rows(n, share), ld_x, h_in)) ||
                  ranges_overlap(dW, dw_bytes, dy, matrix_bytes(n, ld_dy, h_out)))))
     return SGMV_ERR_ALIAS;
-  if (static_cast<int64_t>(n_groups) * (h_out / 64 + 8) * (h_in / 64 + 8) > INT32_MAX)
-    return SGMV_ERR_SHAPE;
+  const Launch L = dw_launch(n_groups, h_in, h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
   if ((st = check_device())) return st;
   TileArgs A{};
   A.T = {starts, perm, n, n_groups};
@@ -245,6 +246,5 @@ extern "C" int sgmv_group_matmul_dw(hipStream_t stream, int32_t dtype, void* dW,
   A.out = static_cast<uint16_t*>(dW);
   A.ld_r = 2 * ld_dy, A.ld_c = 2 * ld_x, A.ld_out = h_in, A.out_group = dW_stride;
   A.rows = h_out, A.cols = h_in;
-  const Launch L = dw_launch(n_groups, h_in, h_out);
   return hip_status(perm ? launch_tiles<kDw, true>(dtype, stream, A, L) : launch_tiles<kDw, false>(dtype, stream, A, L));
 }

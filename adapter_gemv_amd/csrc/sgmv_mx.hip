@@ -121,8 +121,10 @@ inline uint32_t mx_grid(const MxSpan& S) {
   return static_cast<uint32_t>((S.pieces + 256 * kMxPer - 1) / (256 * kMxPer));
 }
 
+constexpr int64_t kMxMost = (int64_t(1) << 24) - 1;  // workgroups of 256 threads in a grid
+
 inline int check_mx_rows(int64_t rows, int32_t h, int64_t ld) {
-  if (rows < 0 || rows > (int64_t(1) << 40) / h) return SGMV_ERR_SHAPE;
+  if (rows < 0 || rows > kMxMost * (256 * kMxPer * 8) / h) return SGMV_ERR_SHAPE;
   if (h % kMxBlock != 0 || ld % 8 != 0) return SGMV_ERR_ALIGNMENT;
   return h < kMxBlock || h > kMaxDim || ld < h ? SGMV_ERR_SHAPE : SGMV_OK;
 }
@@ -195,7 +197,7 @@ inline int check_mx_product(int32_t dtype, const void* y, int64_t ld_y, int32_t 
   if (over_tables(y, y_bytes, starts, perm, n, G) || ranges_overlap(y, y_bytes, W_codes, elems / 2) ||
       ranges_overlap(y, y_bytes, W_scales, elems / 32))
     return SGMV_ERR_ALIAS;
-  return tiles_fit(n, G, starts, h_out) ? SGMV_OK : SGMV_ERR_SHAPE;
+  return SGMV_OK;
 }
 
 }  // namespace
@@ -212,8 +214,9 @@ extern "C" int sgmv_mx_matmul(hipStream_t stream, int32_t dtype, void* y, int64_
   if (!aligned16(x)) return SGMV_ERR_ALIGNMENT;
   if (ranges_overlap(y, matrix_bytes(n, ld_y, h_out), x, matrix_bytes(shared_rows(n, share), ld_x, h_in)))
     return SGMV_ERR_ALIAS;
-  if ((st = check_device())) return st;
   const Launch L = rows_launch(kMxW, n, n_groups, starts, h_in, h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
   if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};
@@ -253,8 +256,9 @@ extern "C" int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void*
   const size_t elems = static_cast<size_t>(shared_rows(n, share)) * h_in;
   if (ranges_overlap(y, y_bytes, x_codes, elems / 2) || ranges_overlap(y, y_bytes, x_scales, elems / 32))
     return SGMV_ERR_ALIAS;
-  if ((st = check_device())) return st;
   const Launch L = rows_launch(kMxBoth, n, n_groups, starts, h_in, h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
+  if ((st = check_device())) return st;
   if (L.rows == kSkinnyRows) {
     SkinnyArgs S{};
     S.T = {starts, perm, n, n_groups};

@@ -48,12 +48,6 @@ inline int64_t max_row_tiles(int32_t n, int32_t G, bool grouped, int BM) {
   return most < n ? most : n;
 }
 
-// whether the tiles of a product of n rows and `cols` columns can be launched, at the smallest
-// tile
-inline bool tiles_fit(int32_t n, int32_t G, bool grouped, int32_t cols) {
-  return max_row_tiles(n, G, grouped, 16) * (cols / 16 + 8) <= INT32_MAX;
-}
-
 inline size_t pool_bytes16(int32_t G, int64_t stride, int64_t elems) {
   return 2 * (static_cast<size_t>(G - 1) * static_cast<size_t>(stride) + static_cast<size_t>(elems));
 }
@@ -65,6 +59,7 @@ constexpr int kTileXcds = 8;  // workgroups of tiles come in whole rounds of the
 struct Launch {
   int rows, cols, waves;
   int64_t workgroups;
+  bool fits() const { return workgroups * 64 * waves <= UINT32_MAX; }  // the threads of a grid
 };
 
 inline int64_t tiles_of(int64_t n, int size) { return (n + size - 1) / size; }

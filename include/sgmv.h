@@ -447,9 +447,12 @@ int sgmv_lora_add_host_ids_noalloc(hipStream_t stream, int32_t dtype, void* y, i
  * n rows one group in caller order: a dense product.
  *
  * These calls need no workspace.  Their errors are those of the other calls: SGMV_ERR_SHAPE
- * (also for n > 2^30, share < 1, n * share >= 2^31 and products of more than 2^31 - 1 tiles), SGMV_ERR_ALIGNMENT,
- * SGMV_ERR_NULL, SGMV_ERR_UNSUPPORTED (dtype; n_groups above SGMV_MAX_GROUPS),
- * SGMV_ERR_ALIAS (an output overlaps an input, the tables among them), SGMV_ERR_HIP.
+ * (also for n > 2^30, share < 1, n * share >= 2^31, and a launch that would have 2^32 threads:
+ * about 16 to an output column for each group and each 32 rows, so a thousand groups of 2^17
+ * columns are fewer),
+ * SGMV_ERR_ALIGNMENT, SGMV_ERR_NULL, SGMV_ERR_UNSUPPORTED (dtype; n_groups above
+ * SGMV_MAX_GROUPS), SGMV_ERR_ALIAS (an output overlaps an input, the tables among them),
+ * SGMV_ERR_HIP.
  */
 #define SGMV_MAX_GROUPS 1024
 

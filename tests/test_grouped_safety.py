@@ -151,3 +151,25 @@ def test_one_row_of_any_stride(monkeypatch):
     assert len(calls) == 3 * 6
     for name, args in calls:
         assert all(args[at] == ld for at, ld in strides[name]), (name, args)
+
+
+def test_launches_past_the_threads_of_a_grid_are_refused():
+    """A grid has fewer than 2^32 threads; products of more, which only many groups of very wide
+    weights reach, are refused with the code that the header names, not by the launch."""
+    wide = dict(n=1024, n_groups=1024)
+    for name, args, _, _ in PRODUCTS:
+        call = getattr(_lib.lib(), name)
+        if name == "sgmv_group_matmul":
+            kw = dict(ld_y=1 << 22, ld_x=8, W_stride=1 << 25, h_in=8, h_out=1 << 22)
+        elif name == "sgmv_group_matmul_dx":
+            kw = dict(ld_dx=1 << 22, ld_dy=8, W_stride=1 << 25, h_in=1 << 22, h_out=8)
+        elif name == "sgmv_group_matmul_dw":
+            kw = dict(dW_stride=1 << 40, ld_x=1 << 19, ld_dy=1 << 21, h_in=1 << 19, h_out=1 << 21,
+                      x=X << 12, dy=Y << 12, starts=STARTS << 12, perm=PERM << 12)
+        else:
+            kw = dict(ld_y=1 << 22, h_in=32, h_out=1 << 22)
+            if "ld_x" in args:
+                kw["ld_x"] = 32
+        assert call(*{**args, **wide, **kw}.values()) == _lib.ERR_SHAPE, name
+    for call in (_lib.lib().sgmv_mx_quantize, _lib.lib().sgmv_mx_dequantize):
+        assert call(None, 1, X, X << 4, X << 8, 256, 1 << 29, 256) == _lib.ERR_SHAPE
