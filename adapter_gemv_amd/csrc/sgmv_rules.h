@@ -64,24 +64,6 @@ struct Launch {
 
 inline int64_t tiles_of(int64_t n, int size) { return (n + size - 1) / size; }
 
-// Whether few rows meet each weight, so that streaming beats tiles: the smaller of two estimates,
-// in microseconds.  Both were fitted to 1 to 64 groups of 8 to 256 rows (weights 4096 x 1024 to
-// 5120 x 13824).  Streaming takes 0.38 to 0.5 us (16-bit) or 0.17 to 0.26 us (4-bit) for a million
-// weights and row tile, the less where the rows are at most 16.  Tiles of 128 x 128 take 0.56 us
-// (4-bit: 0.8 us) for 64 contracted elements and round of the card, and for 16-bit weights no less
-// than the stream at 4.3 TB/s.  Of groups only the mean size is known: each is taken to end in
-// half a tile.
-inline bool few_rows(int32_t n, int32_t G, int32_t h_in, int32_t h_out, bool mx) {
-  const double met = std::min(n, G), weights = 1e-6 * h_in * h_out;
-  const auto tiles = [&](double B) { return G == 1 ? std::ceil(n / B) : std::max(met, n / B + met / 2); };
-  const bool small = n <= 16 * met;
-  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.17 : 0.26) : (small ? 0.38 : 0.5));
-  const double tiles128 = tiles(128) * std::ceil(h_out / 128.0), steps = h_in / 64.0;
-  const double tiled = mx ? 0.8 * steps * std::max(1.0, tiles128 / 320)
-                          : std::max(0.56 * steps * std::max(1.0, tiles128 / 512), met * weights * 2 / 4.3);
-  return stream < tiled;
-}
-
 // Columns and wavefronts of a workgroup.  16-bit weights: 16 columns, 4 wavefronts (64 experts of
 // 4096 x 1024, 32 rows: 38 us; 40 with 8 wavefronts, 44 with 32 columns).
 // 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
@@ -93,6 +75,47 @@ inline Launch skinny_launch(int32_t n, int32_t G, bool grouped, int32_t h_out, b
   const int64_t row_tiles = max_row_tiles(n, G, grouped, kSkinnyRows);
   const int cols = mx && row_tiles * (h_out / 32) >= 256 ? 32 : 16;
   return {kSkinnyRows, cols, !mx ? 4 : cols == 32 ? 2 : 8, row_tiles * tiles_of(h_out, cols)};
+}
+
+// Whether few rows meet each weight, so that streaming beats tiles: the smaller of two estimates,
+// in microseconds, fitted to 1 to 64 groups of 1 to 512 rows (weights 4096 x 1024 to 5120 x 13824, and
+// with both sides in 4 bits from 1024 x 1024).  Of groups only the mean size is known: each is taken
+// to end in half a tile.
+// Streaming takes 0.38 to 0.5 us (16-bit) or 0.17 to 0.26 us (4-bit weights) for a million weights
+// and row tile, the less where the rows are at most 16.  Tiles of 128 x 128 take 0.56 us (4-bit
+// weights: 0.8 us) for 64 contracted elements and round of the card, and for 16-bit weights no less
+// than the stream at 4.3 TB/s.
+// With both sides in 4 bits tiles take 0.64 us for 256 contracted elements and round, and no less
+// than the stream at 4.3 TB/s: a fifth of what tiles with converted weights take, so that streaming
+// pays only while it is short of workgroups as well.  It then takes 1.15 to 3.8 us for 1024
+// contracted elements, by rows and form, or 0.12 to 0.18 us for a million weights.
+// Measured, streaming against tiles, us:     16-bit         4-bit weights   both sides in 4 bits
+//   2048 x 2048, 16 rows                                                    7.6   8.2
+//   4096 x 4096, 16 rows                     8.9   36.9     9.5   44.4      10.0  13.0
+//   4096 x 4096, 64 rows                     20.6  38.3     17.7  44.4      20.1  13.3
+//   4096 x 4096, 256 rows                    68.4  38.6     37.9  44.5      39.7  13.8
+//   8192 x 1024, 128 rows                    26.9  68.5     20.1  84.7      21.5  22.9
+//   5120 x 13824, 64 rows                    75.4  49.2     46.0  55.4      49.5  18.1
+//   8 of 5120 x 13824, 16 rows each          261   266      113   246       107   92
+//   64 of 4096 x 1024, 16 rows each          108   128      55.6  71.5      55.0  27.9
+inline bool few_rows(sgmv_dev::Mode M, int32_t n, int32_t G, bool grouped, int32_t h_in, int32_t h_out) {
+  const double met = std::min(n, G), weights = 1e-6 * h_in * h_out;
+  const auto tiles = [&](double B) { return G == 1 ? std::ceil(n / B) : std::max(met, n / B + met / 2); };
+  const bool small = n <= 16 * met;
+  const double tiles128 = tiles(128) * std::ceil(h_out / 128.0), steps = h_in / 64.0;
+  if (M == sgmv_dev::kMxBoth) {
+    const Launch L = skinny_launch(n, G, grouped, h_out, true);
+    const double length = L.waves == 8 ? (small ? 1.15 : 2.0) * std::max(1.0, L.workgroups / 256.0)
+                                       : (small ? 1.6 : 3.8);
+    const double million = small ? 0.12 + 0.004 * n / met : 0.26;
+    return 4.5 + std::max(length * h_in / 1024, tiles(32) * weights * million) <
+           std::max(3.5 + 0.16 * steps * std::max(1.0, tiles128 / 320), met * weights * 0.53 / 4.3);
+  }
+  const bool mx = M == sgmv_dev::kMxW;
+  const double stream = 8 + tiles(32) * weights * (mx ? (small ? 0.17 : 0.26) : (small ? 0.38 : 0.5));
+  const double tiled = mx ? 0.8 * steps * std::max(1.0, tiles128 / 320)
+                          : std::max(0.56 * steps * std::max(1.0, tiles128 / 512), met * weights * 2 / 4.3);
+  return stream < tiled;
 }
 
 // Tile size.  256 x 256 (one workgroup to a CU) runs full tiles at 1.3 times the rate of
@@ -126,7 +149,7 @@ int mx_tile(F tiles) {
 // rows of none, times column tiles.
 inline Launch rows_launch(sgmv_dev::Mode M, int32_t n, int32_t G, bool grouped, int32_t h_in, int32_t h_out) {
   const bool mx = M == sgmv_dev::kMxW || M == sgmv_dev::kMxBoth;
-  if (M != sgmv_dev::kDx && few_rows(n, G, h_in, h_out, mx)) return skinny_launch(n, G, grouped, h_out, mx);
+  if (M != sgmv_dev::kDx && few_rows(M, n, G, grouped, h_in, h_out)) return skinny_launch(n, G, grouped, h_out, mx);
   const int32_t out = M == sgmv_dev::kDx ? h_in : h_out;
   const auto expected = [&](int BR, int BC) {
     const double rows = n;

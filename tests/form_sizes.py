@@ -27,8 +27,12 @@ MX_WIDE = [(8, 1, 3, 2080, 3000), (60, 1, 3, 2080, 3000), (5, 1, 0, 2080, 8200),
 # and in tiles, 16-bit rows
 MX_TILES = {TILE_128: [(300, 1, 0, 160, 264)], TILE_HALF: [(1100, 1, 0, 160, 7000)],
             TILE_256: [(4096, 1, 0, 160, 4096), (3600, 1, 2, 96, 4088), (3600, 1, 2, 544, 4088)]}
-# both sides in 4 bits
-MX_BOTH_TILES = {TILE_128: [(300, 1, 0, 160, 264)], TILE_256: [(4096, 1, 0, 160, 4096)]}
+# both sides in 4 bits: streamed only where few rows meet long weights (15 rows to a group on
+# average are more than 16 in many)
+BOTH_DEEP = [(4, 1, 3, 8224, 72), (60, 1, 3, 8224, 72), (20, 2, 5, 8416, 264), (1, 1, 0, 4128, 264),
+             (24, 1, 0, 8416, 264)]
+BOTH_WIDE = [(300, 1, 20, 6176, 296), (5, 1, 0, 5152, 8200)]
+BOTH_TILES = {TILE_128: [(300, 1, 0, 160, 264)], TILE_256: [(4096, 1, 0, 160, 4096)]}
 
 
 def cases():
@@ -36,12 +40,12 @@ def cases():
     forward, mx, both = "forward", "mx", "both"
     for size in [*STREAMED, STREAMED_FAR, *STREAMED_MIXED, *STREAMED_REPEATED]:
         yield forward, size, STREAM_16
-    for mode in (mx, both):
-        for size in MX_DEEP:
+    for mode, deep, wide in ((mx, MX_DEEP, MX_WIDE), (both, BOTH_DEEP, BOTH_WIDE)):
+        for size in deep:
             yield mode, size, STREAM_4_DEEP
-        for size in MX_WIDE:
+        for size in wide:
             yield mode, size, STREAM_4_WIDE
-    for mode, tiles in ((mx, MX_TILES), (both, MX_BOTH_TILES)):
+    for mode, tiles in ((mx, MX_TILES), (both, BOTH_TILES)):
         for form, sizes in tiles.items():
             for size in sizes:
                 yield mode, size, form

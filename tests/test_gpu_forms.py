@@ -160,7 +160,7 @@ def test_streamed_same_bits_and_graph_replay(torch, size):
 # --------------------------------------------------------------------------------------
 # 4-bit weights, in every form
 # --------------------------------------------------------------------------------------
-MX = [*F.MX_DEEP, *F.MX_WIDE, *(s for sizes in F.MX_TILES.values() for s in sizes)]
+MX = [*F.MX_DEEP, *F.MX_WIDE, *F.BOTH_DEEP, *F.BOTH_WIDE, *(s for sizes in F.MX_TILES.values() for s in sizes)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -230,7 +230,8 @@ def test_mx_what_is_not_finite_stays_where_it_is(torch, size, dtype):
 
 
 @pytest.mark.parametrize("both", [False, True], ids=["x16", "x4"])
-@pytest.mark.parametrize("size", [F.MX_DEEP[2], F.MX_WIDE[1], F.MX_TILES[F.TILE_256][1]],
+@pytest.mark.parametrize("size", [F.MX_DEEP[2], F.MX_WIDE[1], F.MX_TILES[F.TILE_256][1], F.BOTH_DEEP[2],
+                                  F.BOTH_WIDE[0]],
                          ids=lambda s: "x".join(map(str, s)))
 def test_mx_same_bits_and_graph_replay(torch, size, both):
     import adapter_gemv_amd as sgmv

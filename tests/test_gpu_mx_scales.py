@@ -11,9 +11,10 @@ from oracle import grouped_oracle as G
 pytestmark = pytest.mark.gpu
 
 # rows, h_in, h_out: the streaming kernels of 8 wavefronts and of 32 columns with 16 rows and with
-# 32, then the tiled kernels of 128 x 128, 128 x 256 and 256 x 256
+# 32, then the tiled kernels of 128 x 128, 128 x 256 and 256 x 256; the last two are for the
+# streaming kernels with both sides in 4 bits
 SIZES = [(3, 2080, 264), (24, 2304, 264), (5, 2080, 8200), (24, 2304, 8200), (300, 160, 264),
-         (1100, 160, 7000), (4096, 160, 4096)]
+         (1100, 160, 7000), (4096, 160, 4096), (24, 8416, 264), (5, 5152, 8200)]
 
 
 @pytest.fixture(scope="module")

@@ -59,5 +59,31 @@ def test_tiled_forms_of_16_bit_weights(form_of):
 def test_sizes_of_the_scale_tests(form_of):
     from test_gpu_mx_scales import SIZES
     got = form_of([("mx", (rows, 1, 0, h_in, h_out)) for rows, h_in, h_out in SIZES])
-    assert [f[:3] for f in got] == [F.STREAM_4_DEEP] * 2 + [F.STREAM_4_WIDE] * 2 + [F.TILE_128, F.TILE_HALF,
-                                                                                    F.TILE_256]
+    assert [f[:3] for f in got] == [F.STREAM_4_DEEP] * 2 + [F.STREAM_4_WIDE] * 2 + [
+        F.TILE_128, F.TILE_HALF, F.TILE_256, F.STREAM_4_DEEP, F.STREAM_4_WIDE]
+    got = form_of([("both", (rows, 1, 0, h_in, h_out)) for rows, h_in, h_out in SIZES])
+    assert [f[:3] for f in got[4:]] == [F.TILE_128, F.TILE_128, F.TILE_256, F.STREAM_4_DEEP, F.STREAM_4_WIDE]
+
+
+def test_the_form_that_measured_faster_is_taken(form_of):
+    """Both forms timed (us, streaming and tiles) where they differ by more than a tenth."""
+    measured = [
+        # mode, (rows, share, groups, h_in, h_out), streaming, tiles
+        ("forward", (16, 1, 0, 4096, 4096), 8.9, 36.9), ("forward", (64, 1, 0, 4096, 4096), 20.6, 38.3),
+        ("forward", (256, 1, 0, 4096, 4096), 68.4, 38.6), ("forward", (256, 1, 0, 8192, 1024), 36.4, 71.7),
+        ("forward", (64, 1, 0, 5120, 13824), 75.4, 49.2), ("forward", (128, 1, 8, 4096, 1024), 16.6, 39.0),
+        ("forward", (256, 1, 8, 5120, 13824), 347.5, 214.2), ("forward", (2048, 1, 64, 4096, 1024), 151.9, 124.9),
+        ("mx", (16, 1, 0, 4096, 4096), 9.5, 44.4), ("mx", (256, 1, 0, 4096, 4096), 37.9, 44.5),
+        ("mx", (512, 1, 0, 4096, 4096), 73.1, 45.6), ("mx", (512, 1, 0, 8192, 1024), 40.2, 85.0),
+        ("mx", (64, 1, 0, 5120, 13824), 46.0, 55.4), ("mx", (128, 1, 0, 5120, 13824), 86.4, 56.6),
+        ("mx", (1024, 1, 8, 4096, 1024), 39.6, 45.9), ("mx", (128, 1, 8, 5120, 13824), 112.7, 245.7),
+        ("mx", (1024, 1, 64, 4096, 1024), 55.6, 71.5), ("mx", (2048, 1, 64, 4096, 1024), 80.0, 71.8),
+        ("both", (16, 1, 0, 4096, 4096), 10.0, 13.0), ("both", (64, 1, 0, 4096, 4096), 20.1, 13.3),
+        ("both", (256, 1, 0, 4096, 4096), 39.7, 13.8), ("both", (16, 1, 0, 8192, 1024), 13.7, 22.4),
+        ("both", (256, 1, 0, 8192, 1024), 35.5, 23.0), ("both", (16, 1, 0, 5120, 13824), 19.2, 17.0),
+        ("both", (64, 1, 0, 5120, 13824), 49.5, 18.1), ("both", (256, 1, 8, 4096, 1024), 22.2, 14.0),
+        ("both", (128, 1, 8, 5120, 13824), 107.0, 92.0), ("both", (1024, 1, 64, 4096, 1024), 55.0, 27.9),
+    ]
+    got = form_of([(mode, size) for mode, size, _, _ in measured])
+    wrong = [m for m, form in zip(measured, got) if (form[0] == F.STREAM_16[0]) != (m[2] < m[3])]
+    assert not wrong, wrong
