@@ -68,7 +68,7 @@ inline int64_t tiles_of(int64_t n, int size) { return (n + size - 1) / size; }
 // 4096 x 1024, 32 rows: 38 us; 40 with 8 wavefronts, 44 with 32 columns).
 // 4-bit weights, of whose rows a wavefront has a quarter of the bytes: 32 columns, 2 wavefronts
 // (8 experts of 5120 x 13824, 32 rows, in the first form: 93 us; 104 with 4 wavefronts, 124 with 16
-// columns; the call is now at 89), or 16 columns and 8 wavefronts where that leaves CUs without work
+// columns; the call is now at 85 to 92), or 16 columns and 8 wavefronts where that leaves CUs without work
 // (now, the first and the second: 4096 x 4096, 32 rows, 17.5 and 12.1 us; 64 rows 17.9 and 22.2;
 // 4096 x 8192, 32 rows, 17.7 and 22.1; 5120 x 13824, 16 rows, 18.7 and 37.5).
 inline Launch skinny_launch(int32_t n, int32_t G, bool grouped, int32_t h_out, bool mx) {

@@ -466,7 +466,7 @@ struct Skinny {
 
   // Every LDS read of this wavefront has returned.  The buffer that a step fills is the one the
   // step before read, and a load into LDS is not held back by reads in flight.  (64 experts of
-  // 4096 x 1024, 32 x 2 rows, with it: 66 us a call.)
+  // 4096 x 1024, 32 x 2 rows, with it: 66 to 70 us a call.)
   static __device__ __forceinline__ void wait_reads() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt 0

@@ -12,6 +12,10 @@ computed here::
 
 ``share`` is how many consecutive rows read one row of x (the experts per token): the rows
 of the other operand over the rows of x.
+
+The calls write into tensors, like the LoRA calls, and automatic differentiation does not see
+them: a training program calls the two gradients itself, or wraps the three products in a
+``torch.autograd.Function``.  Work given to a ``stream`` is ordered on that stream alone.
 """
 from __future__ import annotations
 
