@@ -11,3 +11,9 @@ from .grouped import (  # noqa: F401
     RowGroups, group_matmul, group_matmul_dw, group_matmul_dx, group_rows,
 )
 from .mx import MxTensor, mx_dequantize, mx_matmul, mx_quantize  # noqa: F401
+from .routing import (  # noqa: F401
+    Routes, combine_rows, combine_rows_backward, route, route_backward,
+)
+from .fp8 import (  # noqa: F401
+    Fp8Rows, Fp8Weight, fp8_dequantize, fp8_matmul, fp8_matmul_dx, fp8_quantize, fp8_quantize_weight,
+)

@@ -9,6 +9,10 @@ from .build import LIB_PATH, PHASES_LIB_PATH
 
 F16 = 0
 BF16 = 1
+F32 = 2
+
+SOFTMAX = 0
+SIGMOID = 1
 
 OK = 0
 ERR_NULL = 1
@@ -96,6 +100,27 @@ SIGNATURES["sgmv_mx_matmul"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _i3
 SIGNATURES["sgmv_mx_matmul_quantized"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i32, _p,
                                                          _p, _p, _p, _i32, _i32, _i32, _i32])
 MAX_GROUPS = 1024
+
+# routing to experts, the weighted sum of their rows, and 8-bit products in blocks of 128
+_f32 = ctypes.c_float
+SIGNATURES["sgmv_route"] = (ctypes.c_int, [_p, _i32, _p, _p, _p, _i64, _p, _i32, _i32, _i32, _i32, _i32,
+                                           _i32, _i32, _i32, _f32])
+SIGNATURES["sgmv_route_backward"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i64, _p, _i32, _i32, _i32,
+                                                    _i32, _i32, _f32])
+SIGNATURES["sgmv_combine_rows"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _p, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_combine_rows_backward"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i64, _p, _i64, _p,
+                                                           _i32, _i32, _i32])
+SIGNATURES["sgmv_block_quantize"] = (ctypes.c_int, [_p, _i32, _p, _p, _p, _i64, _i64, _i32])
+SIGNATURES["sgmv_block_dequantize"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i64, _i32])
+SIGNATURES["sgmv_block_quantize_weight"] = (ctypes.c_int, [_p, _i32, _p, _p, _p, _i64, _i32, _i32, _i32])
+SIGNATURES["sgmv_block_dequantize_weight"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i32, _i32, _i32])
+SIGNATURES["sgmv_block_workspace_bytes"] = (_sz, [_i32, _i32, _i32, _i32, _i32, _i32])
+SIGNATURES["sgmv_block_dx_workspace_bytes"] = (_sz, [_i32, _i32])
+_tail = [_p, _p, _p, _p, _i32, _i32, _i32, _i32]   # the weight, the tables and the sizes
+SIGNATURES["sgmv_block_matmul"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, _i32, *_tail, _p, _sz])
+SIGNATURES["sgmv_block_matmul_quantized"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, _i32, *_tail])
+SIGNATURES["sgmv_block_matmul_dx"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _i64, *_tail, _p, _sz])
+SIGNATURES["sgmv_block_matmul_dx_quantized"] = (ctypes.c_int, [_p, _i32, _p, _i64, _p, _p, *_tail])
 
 _LIB = None
 _PATH = LIB_PATH

@@ -26,7 +26,7 @@ PHASES_LIB_PATH = os.path.join(PKG, "libsgmv_phases.so")
 ARCH = "gfx950"
 
 SOURCES = ["sgmv_segments.cpp", "sgmv_cache.cpp", "sgmv_kernels.hip", "sgmv_decode.hip",
-           "sgmv_group.hip", "sgmv_mx.hip"]
+           "sgmv_group.hip", "sgmv_mx.hip", "sgmv_route.hip", "sgmv_fp8.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", f"-I{INCLUDE}",
           "-Wall", "-Wno-unused-function",

@@ -77,6 +77,7 @@ extern "C" {
 /* element types of x, y, A, B */
 #define SGMV_F16 0
 #define SGMV_BF16 1
+#define SGMV_F32 2 /* the logits of sgmv_route and their gradient alone */
 
 /* status codes */
 #define SGMV_OK 0
@@ -532,6 +533,156 @@ int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t
                              const void* W_codes, const void* W_scales, const int32_t* starts,
                              const int32_t* perm, int32_t n, int32_t n_groups, int32_t h_in,
                              int32_t h_out);
+
+/*
+ * Routing to experts: the ids that sgmv_group_rows takes, from the logits of a router.  With
+ * l the logits of one of n tokens and E experts,
+ *
+ *     s = softmax(l) (SGMV_SOFTMAX) or 1 / (1 + exp(-l)) (SGMV_SIGMOID)
+ *     c = s + bias                                   (the values that choose; bias NULL: s)
+ *
+ * the experts lie in expert_groups equal runs.  A group's score is the sum of its group_best
+ * (1 or 2) largest c; the keep_groups groups of the largest score stay, and of their experts
+ * the k with the largest c are chosen: ids[t, 0 .. k) in order of c, and
+ *
+ *     weights[t, j] = scale * s[ids[t, j]]           (/ the sum of the chosen s: normalize)
+ *
+ * Where values are equal the lowest group or expert goes first; the order is that of the exact
+ * values, whatever float32 makes of them.  An expert whose l or c is minus infinity is never
+ * chosen (a group counts those it has left, and stays only if it has one); places without an
+ * expert get the id -1, which belongs to no group, and the weight 0: a padded token is a row of
+ * minus infinities.  NaN ranks above all values, and one NaN (softmax: also one plus infinity)
+ * makes every s of a softmax NaN, or the one s of a sigmoid; weights that depend on it are NaN.
+ *   logits   SGMV_F16, SGMV_BF16 or SGMV_F32 [n, n_experts], rows ld_logits elements apart (any
+ *            number, not less than n_experts)
+ *   bias     float32 [n_experts] or NULL
+ *   ids      int32 [n, k] out; weights float32 [n, k] out; both dense
+ * 1 <= n_experts <= SGMV_MAX_GROUPS; 1 <= k <= n_experts, at most SGMV_MAX_ROUTES; expert_groups
+ * divides n_experts and is at most SGMV_MAX_EXPERT_GROUPS; 1 <= keep_groups <= expert_groups.
+ */
+#define SGMV_SOFTMAX 0
+#define SGMV_SIGMOID 1
+#define SGMV_MAX_ROUTES 64
+#define SGMV_MAX_EXPERT_GROUPS 64
+
+int sgmv_route(hipStream_t stream, int32_t dtype, int32_t* ids, float* weights, const void* logits,
+               int64_t ld_logits, const float* bias, int32_t n, int32_t n_experts, int32_t k,
+               int32_t expert_groups, int32_t keep_groups, int32_t group_best, int32_t scores,
+               int32_t normalize, float scale);
+
+/*
+ * The gradient of the logits from that of the weights, the chosen experts held fixed (a bias
+ * and groups take no part).  With g[j] = scale * dweights[t, j], s_j = s[ids[t, j]], and u_j =
+ * s_j / (sum of the chosen s):
+ *
+ *     softmax              dl_i = s_i * ((sum of g_j with ids[t, j] = i) - sum_j g_j s_j)
+ *     softmax, normalize   dl_i = sum over j with ids[t, j] = i: u_j (g_j - sum_m g_m u_m)
+ *     sigmoid              dl_i = the same of g_j s_j (1 - s_j)
+ *     sigmoid, normalize   dl_i = the same of u_j (1 - s_j) (g_j - sum_m g_m u_m)
+ *
+ * With normalize only the chosen logits are read (u is the softmax of these), so that a NaN
+ * elsewhere in the row does not show.  Every element of dlogits [n, n_experts] (dtype, rows ld_dlogits apart) is written.  Places
+ * whose id lies outside [0, n_experts) take no part, nor does an expert whose logit is minus
+ * infinity: its gradient is zero.
+ */
+int sgmv_route_backward(hipStream_t stream, int32_t dtype, void* dlogits, int64_t ld_dlogits,
+                        const float* dweights, const void* logits, int64_t ld_logits,
+                        const int32_t* ids, int32_t n, int32_t n_experts, int32_t k,
+                        int32_t scores, int32_t normalize, float scale);
+
+/*
+ * The k rows of each token summed with its weights, as they come out of the products above:
+ *
+ *     out[t, :]         = sum_j weights[t, j] * y[t * k + j, :]       (plus out: add != 0)
+ *     dy[t * k + j, :]  = weights[t, j] * dout[t, :]                  (..._backward)
+ *     dweights[t, j]    = sum over the columns of dout[t] * y[t * k + j]
+ *
+ * weights == NULL: ones (the gradient of a row that k rows share is their sum); then the
+ * backward call takes no dweights.  weights and dweights float32 [n, k], dense; the others dtype,
+ * [n, h] or [n * k, h] with strides and alignment as for the products.  Sums are float32, each
+ * output is rounded once.  k >= 1, n * k <= 2^30.  An output may overlap no input, except that out
+ * is its own input with add.
+ */
+int sgmv_combine_rows(hipStream_t stream, int32_t dtype, void* out, int64_t ld_out, const void* y,
+                      int64_t ld_y, const float* weights, int32_t n, int32_t k, int32_t h,
+                      int32_t add);
+
+int sgmv_combine_rows_backward(hipStream_t stream, int32_t dtype, void* dy, int64_t ld_dy,
+                               float* dweights, const void* dout, int64_t ld_dout, const void* y,
+                               int64_t ld_y, const float* weights, int32_t n, int32_t k, int32_t h);
+
+/*
+ * 8-bit floating point with a scale for each block of 128 (the library's "block" format): one sign, four exponent and three
+ * mantissa bits (0x00 .. 0x7e are 0, then 2^-9 up to 448; 0x7f is NaN; + 0x80 the negative), and
+ * float32 scales of any value.  h is a multiple of 16 and need not be one of 128: the last block
+ * is shorter.
+ *   rows     codes uint8 [rows, h], scales float32 [rows, ceil(h / 128)]
+ *   weights  codes uint8 [G, h_out, h_in], scales float32 [G, ceil(h_out / 128),
+ *            ceil(h_in / 128)]: one for each 128 x 128
+ * all dense, codes 16-byte aligned.  An element is its code's value times its block's scale.
+ *
+ * The quantisers take 16-bit values (dtype).  A block's scale is the least power of two, not below
+ * 2^-126, of which 448 times is not below the block's largest magnitude (2^-126 for zeros), so
+ * that quotients are exact and each element is rounded once, to nearest, ties to even.  A block
+ * that holds an infinity or a NaN gets the scale NaN and codes 0.
+ * The dequantisers write the values, rounded once to dtype.
+ */
+int sgmv_block_quantize(hipStream_t stream, int32_t dtype, void* codes, float* scales, const void* x,
+                      int64_t ld_x, int64_t rows, int32_t h);
+
+/* W: n_groups of [h_out, h_in] row-major, W_stride elements apart */
+int sgmv_block_quantize_weight(hipStream_t stream, int32_t dtype, void* codes, float* scales,
+                             const void* W, int64_t W_stride, int32_t n_groups, int32_t h_in,
+                             int32_t h_out);
+
+int sgmv_block_dequantize(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* codes,
+                        const float* scales, int64_t rows, int32_t h);
+
+int sgmv_block_dequantize_weight(hipStream_t stream, int32_t dtype, void* W, int64_t W_stride,
+                               const void* codes, const float* scales, int32_t n_groups,
+                               int32_t h_in, int32_t h_out);
+
+/*
+ * sgmv_group_matmul and sgmv_group_matmul_dx with both sides in this format: x (or dy, along
+ * h_out) is taken to it within the call, exactly as sgmv_block_quantize does, W is in it:
+ *
+ *     y[i, :]  = x8[i / share, :] @ W[g]^T           (sgmv_block_matmul)
+ *     dx[i, :] = dy8[i, :] @ W[g]                    (sgmv_block_matmul_dx)
+ *
+ * The products of a block are summed in float32, times the float32 product of its two scales
+ * (which has to lie in float32's normal range, 2^-126 up to 2^128, to count in full).  The gradient
+ * of the weights is sgmv_group_matmul_dw, of the 16-bit rows.  h_in and h_out are multiples of 16;
+ * everything else is as for the 16-bit calls.
+ *   workspace  device memory, 16-byte aligned, of at least sgmv_block_workspace_bytes of the same
+ *              sizes (0 for some: then it may be NULL), with any contents; its contents after the
+ *              call are of no use.  It may not overlap any operand, and calls that share one must
+ *              be ordered.
+ * The ..._quantized calls take x or dy as sgmv_block_quantize writes it; dtype is the output's.
+ */
+size_t sgmv_block_workspace_bytes(int32_t n, int32_t share, int32_t n_groups, int32_t grouped,
+                                int32_t h_in, int32_t h_out);   /* grouped: starts != NULL */
+size_t sgmv_block_dx_workspace_bytes(int32_t n, int32_t h_out);   /* sgmv_block_matmul_dx */
+
+int sgmv_block_matmul(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* x,
+                    int64_t ld_x, int32_t share, const void* W_codes, const float* W_scales,
+                    const int32_t* starts, const int32_t* perm, int32_t n, int32_t n_groups,
+                    int32_t h_in, int32_t h_out, void* workspace, size_t workspace_bytes);
+
+int sgmv_block_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y,
+                              const void* x_codes, const float* x_scales, int32_t share,
+                              const void* W_codes, const float* W_scales, const int32_t* starts,
+                              const int32_t* perm, int32_t n, int32_t n_groups, int32_t h_in,
+                              int32_t h_out);
+
+int sgmv_block_matmul_dx(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx, const void* dy,
+                       int64_t ld_dy, const void* W_codes, const float* W_scales,
+                       const int32_t* starts, const int32_t* perm, int32_t n, int32_t n_groups,
+                       int32_t h_in, int32_t h_out, void* workspace, size_t workspace_bytes);
+
+int sgmv_block_matmul_dx_quantized(hipStream_t stream, int32_t dtype, void* dx, int64_t ld_dx,
+                                 const void* dy_codes, const float* dy_scales, const void* W_codes,
+                                 const float* W_scales, const int32_t* starts, const int32_t* perm,
+                                 int32_t n, int32_t n_groups, int32_t h_in, int32_t h_out);
 
 #ifdef __cplusplus
 }

@@ -4,3 +4,4 @@ from .sgmv_oracle import (  # noqa: F401
     segments_ranked, lora_add_ranked, DecodedPool, shrink_f64, expand_f64, lora_add_f64,
 )
 from . import grouped_oracle  # noqa: F401
+from . import block_oracle, routing_oracle  # noqa: F401
