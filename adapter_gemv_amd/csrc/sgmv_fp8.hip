@@ -1,6 +1,6 @@
 // 8-bit floating point with a scale for each block of 128: 16-bit values to the format and back,
 // and products with both sides in it.
-#include "sgmv_rows.h"
+#include "sgmv_fp8_tile.h"
 
 using namespace sgmv_dev;
 using namespace sgmv_host;
@@ -9,12 +9,7 @@ namespace {
 
 constexpr int kBlock = 128;
 
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
-typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 typedef __attribute__((ext_vector_type(2))) short s16x2_t;
-typedef __attribute__((ext_vector_type(8))) int i32x8_t;
-
-__host__ __device__ inline int blocks_of(int h) { return (h + kBlock - 1) / kBlock; }
 
 // the larger magnitude of each 16-bit half; magnitudes order like their patterns, infinity and NaN
 // above all
@@ -186,72 +181,27 @@ __global__ __launch_bounds__(256) void fp8_dequantize_weight_kernel(uint16_t* __
 // ------------------------------------------------------------------------------------
 // products
 // ------------------------------------------------------------------------------------
-struct Fp8Args {
-  RowTab T;
-  Share share;
-  const uint8_t* r;       // rows of x or dy
-  const float* r_scale;
-  const uint8_t* w;       // [h_out, h_in]
-  const float* w_scale;
-  uint16_t* out;
-  int64_t ld_out;
-  int32_t h_in, h_out;
-};
-
-// One wavefront makes 16 rows x 16 columns of the output.  The order of a lane's elements along the
-// contracted dimension is the same in both operands, which is all that the instruction needs.
 template <int DT, bool DX>
-__global__ __launch_bounds__(64) void fp8_product_kernel(Fp8Args A) {
-  const int lane = threadIdx.x, l16 = lane & 15, kq = lane >> 4;
-  const int cols = DX ? A.h_in : A.h_out, depth = DX ? A.h_out : A.h_in;
-  const int ct = (cols + 15) / 16, kb = blocks_of(depth), bi = blocks_of(A.h_in);
-  const TileList list(A.T, 16);
-  const int m = blockIdx.x / ct, c0 = (blockIdx.x - m * ct) * 16;
-  if (m >= list.count) return;
-  const RowTile t = list.find(m);
-  const int row = A.T.row(t.row0 + min(l16, t.rows - 1)), col = min(c0 + l16, cols - 1);
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  if (t.g < A.T.G) {
-    const int64_t of = A.share.div(row);
-    const uint8_t* const r = A.r + of * depth;
-    const uint8_t* const w = A.w + static_cast<int64_t>(t.g) * A.h_in * A.h_out;
-    const float* const ws = A.w_scale + static_cast<int64_t>(t.g) * bi * blocks_of(A.h_out);
-    for (int b = 0; b < kb; ++b) {
-      uint32_t rv[8], wv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = b * kBlock + 32 * kq + 4 * i;
-        const bool in = k < depth;  // multiples of 16
-        rv[i] = in ? *reinterpret_cast<const uint32_t*>(r + k) : 0u;
-        wv[i] = 0;
-        if (in && !DX) wv[i] = *reinterpret_cast<const uint32_t*>(w + static_cast<int64_t>(col) * A.h_in + k);
-        if (in && DX)
-          for (int u = 0; u < 4; ++u)
-            wv[i] |= static_cast<uint32_t>(w[static_cast<int64_t>(k + u) * A.h_in + col]) << (8 * u);
-      }
-      i32x8_t a, c;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = static_cast<int>(wv[i]), c[i] = static_cast<int>(rv[i]);
-      const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, c, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0,
-                                                                         0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-      const float s = A.r_scale[of * kb + b] * (DX ? ws[b * bi + min(c0, cols - 1) / kBlock] : ws[c0 / kBlock * bi + b]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
-    }
-  }
-  // lane (l16, kq): row l16, columns 4 * kq .. + 3
-  const int c = c0 + 4 * kq;
-  if (l16 < t.rows && c < cols) {
-    const uint32_t o[2] = {Elem<DT>::pack(acc[0], acc[1]), Elem<DT>::pack(acc[2], acc[3])};
-    store_words<2>(A.out + row * A.ld_out + c, o);
-  }
+hipError_t launch_fp8(hipStream_t s, const Fp8Args& A, const Launch& L) {
+  const uint32_t grid = static_cast<uint32_t>(L.workgroups);
+  if (L.rows == 256) fp8_tile_kernel<DT, DX, 256, 256, 2, 4><<<grid, 512, 0, s>>>(A);
+  else fp8_tile_kernel<DT, DX, 128, 128, 2, 2><<<grid, 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+template <bool DX>
+hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const Launch& L) {
+  return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX>(s, A, L) : launch_fp8<SGMV_BF16, DX>(s, A, L);
 }
 
-template <bool DX>
-hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, int64_t grid) {
-  const auto kernel = dtype == SGMV_F16 ? fp8_product_kernel<SGMV_F16, DX> : fp8_product_kernel<SGMV_BF16, DX>;
-  kernel<<<static_cast<uint32_t>(grid), 64, 0, s>>>(A);
-  return hipGetLastError();
+inline Launch fp8_launch(bool dx, int32_t n, int32_t G, bool grouped, int32_t h_in, int32_t h_out) {
+  const int32_t out = dx ? h_in : h_out;
+  const auto expected = [&](int B) {
+    const double rows = n;
+    return (grouped ? rows / B + 0.5 * std::min(n, G) : std::ceil(rows / B)) * tiles_of(out, B);
+  };
+  const int B = big_tiles(expected(256), expected(128)) ? 256 : 128;
+  const int64_t tiles = max_row_tiles(n, G, grouped, B) * tiles_of(out, B);
+  return {B, B, B == 256 ? 8 : 4, tiles_of(tiles, kTileXcds) * kTileXcds};
 }
 
 // ------------------------------------------------------------------------------------
@@ -393,8 +343,8 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
       (st = check_fp8_dim(P.h_out)) || (st = check_dim(P.cols(), P.ld_out)))
     return st;
   if (!quantized && (st = check_fp8_rows(P.dtype, P.rows(), P.depth(), P.ld_r))) return st;
-  const int64_t grid = max_row_tiles(P.n, P.G, P.starts, 16) * tiles_of(P.cols(), 16);
-  if (grid * 64 > UINT32_MAX) return SGMV_ERR_SHAPE;
+  const Launch L = fp8_launch(P.dx, P.n, P.G, P.starts, P.h_in, P.h_out);
+  if (!L.fits()) return SGMV_ERR_SHAPE;
   if (P.n == 0) return SGMV_OK;
   if (!P.out || !P.r || (quantized && !P.r_scales) || !P.w || !P.w_scales) return SGMV_ERR_NULL;
   if (!aligned16(P.out) || !aligned16(P.r) || !aligned4(P.r_scales) || !aligned16(P.w) || !aligned4(P.w_scales))
@@ -434,7 +384,7 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   A.w_scale = P.w_scales;
   A.out = static_cast<uint16_t*>(P.out);
   A.ld_out = P.ld_out, A.h_in = P.h_in, A.h_out = P.h_out;
-  return hip_status(P.dx ? launch_fp8<true>(P.dtype, stream, A, grid) : launch_fp8<false>(P.dtype, stream, A, grid));
+  return hip_status(P.dx ? launch_fp8<true>(P.dtype, stream, A, L) : launch_fp8<false>(P.dtype, stream, A, L));
 }
 
 }  // namespace

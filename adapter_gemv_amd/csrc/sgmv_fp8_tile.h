@@ -1,0 +1,280 @@
+// The tiled product of 8-bit operands with a scale for each block of 128, by group: rows of x times
+// W^T, or rows of dy times W (DX).
+//
+// A workgroup makes BR rows x BC columns of the output; a stage is one block of the contracted
+// dimension, 128 bytes of each row and column, brought by direct global-to-LDS loads into one of two
+// buffers while the other is multiplied.  An MFMA 16x16x128 takes a whole block; its sums start from
+// zero and are added to the tile's, times the block's two scales: 128 multiply-adds for 32 matrix
+// instructions of a wavefront, which run beside them.
+//
+// x, dy and W lie along their rows where these are contracted: piece c (16 bytes) of tile row q sits
+// in slot c ^ ((q >> 1) & 7), and a fragment is two 16-byte reads.  W of DX lies across: a stage is
+// 128 contracted rows of BC bytes, a fragment four transposing reads (ds_read_b64_tr_b8, each of
+// eight rows of one piece per 16 lanes).  Piece c of row k sits in slot c ^ swizzle(k), so that the 16
+// rows of half a wavefront's read lie over all banks.  A lane has the same contracted positions in both
+// forms: 16 * kq .. + 15 and 64 + 16 * kq .. + 15.
+//
+// Contracted positions past the end are zeros in both operands, tile rows and columns past the end
+// repeat the last one and are not stored.
+#pragma once
+
+#include "sgmv_tile.h"
+
+namespace sgmv_dev {
+
+typedef __attribute__((ext_vector_type(2))) int i32x2_t;
+
+struct Fp8Args {
+  RowTab T;
+  Share share;
+  const uint8_t* r;       // rows of x or dy, dense
+  const float* r_scale;   // [rows, blocks]
+  const uint8_t* w;       // [h_out, h_in]
+  const float* w_scale;   // [blocks of h_out, blocks of h_in]
+  uint16_t* out;
+  int64_t ld_out;
+  int32_t h_in, h_out;
+};
+
+__host__ __device__ inline int blocks_of(int h) { return (h + 127) / 128; }
+
+template <int BR, int BC, int WR, int WC>
+struct Fp8Tile {
+  static constexpr int NW = WR * WC, TH = 64 * NW;
+  static constexpr int NR = BR / WR / 16, NC = BC / WC / 16;  // fragments of a wavefront
+  static constexpr int RI = BR / 8 / NW, CI = BC / 8 / NW;    // loads per stage
+  static_assert(RI * 8 * NW == BR && CI * 8 * NW == BC && NC == 4 && NR % 4 == 0 && RI + CI <= NR * 2, "");
+  static_assert(TH == 2 * BR, "a thread fetches a row's scale of one of two stages");
+  struct RBuf {
+    u32x4_t v[BR * 8];
+  };
+  struct CBuf {
+    u32x4_t v[BC * 8];
+  };
+  struct Scales {
+    alignas(16) float s[2][BR];  // [stage of two][wavefront rows][row of 16][fragment]
+  };
+};
+
+// DX, tiles of B columns: where a piece of contracted row k is moved
+template <int B>
+__device__ inline int swizzle(int k) {
+  static_assert(B == 256 || B == 128, "");
+  return B == 256 ? (k & 7) | (k >> 1 & 8) : (k >> 1 & 3) | (k >> 2 & 4);
+}
+
+template <int DT, bool DX, int BR, int BC, int WR, int WC>
+__global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
+  using C = Fp8Tile<BR, BC, WR, WC>;
+  constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI;
+  __shared__ typename C::RBuf rb0, rb1;
+  __shared__ typename C::CBuf cb0, cb1;
+  __shared__ typename C::Scales sb0, sb1;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
+  const int wr = w / WC, wc = w % WC;
+  const int cols = DX ? A.h_in : A.h_out, depth = DX ? A.h_out : A.h_in, bi = blocks_of(A.h_in);
+
+  // which tile: workgroup b runs on XCD b % 8; each XCD takes a contiguous eighth of the tiles
+  const int ct = (cols + BC - 1) / BC, xcd = blockIdx.x % kTileXcds, at = blockIdx.x / kTileXcds;
+  const TileList list(A.T, BR);
+  const int all = list.count * ct, per = all / kTileXcds, more = all % kTileXcds;
+  if (at >= per + (xcd < more)) return;
+  int m, c0;
+  band_order(xcd * per + min(xcd, more) + at, list.count, ct, &m, &c0);
+  const RowTile t = list.find(m);
+  c0 *= BC;
+  const int nst = t.g == A.T.G ? 0 : blocks_of(depth);  // rows of no group: zeros
+
+  f32x4_t acc[NR][NC];
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const char* const zeros = reinterpret_cast<const char*>(kZeros);
+  const char* const wbase = reinterpret_cast<const char*>(A.w) + static_cast<int64_t>(t.g) * A.h_in * A.h_out;
+  // where this lane's pieces of the first stage are, and how far into the contracted dimension
+  const char *rp[RI], *cp[CI];
+  int rk[RI], ck[CI];
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    const int q = (w * RI + i) * 8 + lane / 8;
+    rk[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
+    const int j = nst ? A.share.div(A.T.row(t.row0 + min(q, t.rows - 1))) : 0;
+    rp[i] = reinterpret_cast<const char*>(A.r) + static_cast<int64_t>(j) * depth + rk[i];
+  }
+#pragma unroll
+  for (int i = 0; i < CI; ++i) {
+    if constexpr (!DX) {
+      const int q = (w * CI + i) * 8 + lane / 8;
+      ck[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
+      cp[i] = wbase + static_cast<int64_t>(min(c0 + q, cols - 1)) * A.h_in + ck[i];
+    } else {
+      constexpr int L = BC / 16;  // lanes to a contracted row
+      ck[i] = (w * CI + i) * (64 / L) + lane / L;
+      cp[i] = wbase + static_cast<int64_t>(ck[i]) * A.h_in + min(c0 + 16 * (lane % L ^ swizzle<BC>(ck[i])), cols - 16);
+    }
+  }
+  auto issue_r = [&](typename C::RBuf& to, int s, auto which) __attribute__((always_inline)) {
+    constexpr int i = decltype(which)::value;
+    to_lds(rk[i] < depth - s * 128 ? rp[i] + static_cast<int64_t>(s) * 128 : zeros, &to.v[(w * RI + i) * 64]);
+  };
+  auto issue_c = [&](typename C::CBuf& to, int s, auto which) __attribute__((always_inline)) {
+    constexpr int i = decltype(which)::value;
+    const char* c = cp[i] + (DX ? static_cast<int64_t>(s) * 128 * A.h_in : static_cast<int64_t>(s) * 128);
+    if constexpr (DX) asm("" : "+v"(c));  // keeps its computation out of a branch
+    to_lds(ck[i] < depth - s * 128 ? c : zeros, &to.v[(w * CI + i) * 64]);
+  };
+  constexpr int LOADS = RI + CI;
+  auto issue_one = [&](typename C::RBuf& rt, typename C::CBuf& ct, int s, auto which) __attribute__((always_inline)) {
+    constexpr int k = decltype(which)::value;
+    if constexpr (k < RI) issue_r(rt, s, which);
+    else issue_c(ct, s, std::integral_constant<int, k - RI>{});
+  };
+
+  // Scales.  Of the rows: this thread's row, for one of two stages; fetched two stages ahead, and
+  // put into LDS behind the products, in the order in which a lane takes them.  Of the weight: one for
+  // the wavefront's columns (a block's, as they are 64 of a multiple of 64) and stage.  Zero past the end.
+  const int sq = tid % BR, ss = tid / BR;
+  const int sto = (sq / (16 * NR) * 16 + sq % 16) * NR + sq / 16 % NR;
+  const int kb = blocks_of(depth);
+  const float* sp = A.r_scale;
+  if (nst) sp += static_cast<int64_t>(A.share.div(A.T.row(t.row0 + min(sq, t.rows - 1)))) * kb;
+  const int cb = min(c0 + wc * 16 * NC, cols - 1) / 128;
+  const float* const wp = A.w_scale + static_cast<int64_t>(t.g) * bi * blocks_of(A.h_out) + (DX ? cb : cb * bi);
+  float sv = 0.f;
+  auto fetch_scales = [&](int s) { sv = global_ptr(sp)[min(s + ss, kb - 1)]; };
+  auto store_scales = [&](typename C::Scales& to, int s) { to.s[ss][sto] = s + ss < nst ? sv : 0.f; };
+  auto w_scale = [&](int s) {
+    const int in = min(s, nst - 1);  // no branch: see the tiled product of 16-bit operands
+    const float v = wp[DX ? static_cast<int64_t>(in) * bi : in];
+    return s < nst ? v : 0.f;
+  };
+
+  // Fragment reads: a lane's offsets, made here, plus constants (so that the compiler tells LDS
+  // buffers apart)
+  int ro[2], co[4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) ro[u] = (wr * NR * 16 + l16) * 8 + ((u * 4 + kq) ^ ((l16 >> 1) & 7));
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int k = 16 * kq + l16 / 2;  // DX: the row whose half piece this lane points at
+    co[u] = DX ? (k * (BC / 16) + ((wc * NC + u) ^ swizzle<BC>(k))) * 2 + (l16 & 1)  // 8-byte pieces
+               : (wc * NC * 16 + l16) * 8 + (((u & 1) * 4 + kq) ^ ((l16 >> 1) & 7));
+  }
+  asm("" : "+v"(ro[0]), "+v"(ro[1]), "+v"(co[0]), "+v"(co[1]), "+v"(co[2]), "+v"(co[3]));
+  auto join = [](u32x4_t a, u32x4_t b) __attribute__((always_inline)) {
+    return i32x8_t{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
+  };
+  auto rfrag = [&](const typename C::RBuf& from, int i) __attribute__((always_inline)) {
+    return join(from.v[ro[0] + i * 128], from.v[ro[1] + i * 128]);
+  };
+  auto cfrag = [&](const typename C::CBuf& from, int j) __attribute__((always_inline)) {
+    if constexpr (!DX) {
+      return join(from.v[co[0] + j * 128], from.v[co[1] + j * 128]);
+    } else {
+      typedef __attribute__((address_space(3))) i32x2_t lds2;
+      const i32x2_t* const p = reinterpret_cast<const i32x2_t*>(from.v) + co[j];
+      i32x8_t v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // rows + 8 * (q & 1) + 64 * (q >> 1)
+        const i32x2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2*)(p + (8 * (q & 1) + 64 * (q >> 1)) * (BC / 8)));
+        v[2 * q] = x.x, v[2 * q + 1] = x.y;
+      }
+      return v;
+    }
+  };
+
+  // One stage: a step for each row fragment, NC MFMAs; the multiply-adds of an MFMA's sums stand two
+  // MFMAs behind it, the next row fragment is read during a step, and each of the first steps issues a
+  // load or two of the next stage.
+  auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb_, const typename C::Scales& sb,
+                   typename C::RBuf& rn, typename C::CBuf& cn, int s, auto half, float ws) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value;
+    constexpr int PER = (LOADS + NR - 1) / NR;
+    i32x8_t cv[NC], rv[2];
+    f32x4_t sum[4];
+    float sc[NR];
+    {
+      const f32x4_t* const from = reinterpret_cast<const f32x4_t*>(&sb.s[H][(wr * 16 + l16) * NR]);
+#pragma unroll
+      for (int i = 0; i < NR / 4; ++i) {
+        const f32x4_t v = from[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sc[4 * i + q] = v[q];
+      }
+    }
+    rv[0] = rfrag(rb, 0);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) cv[j] = cfrag(cb_, j);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) sc[i] *= ws;
+    auto add = [&](auto which) __attribute__((always_inline)) {  // the n-th MFMA's sums
+      constexpr int n = decltype(which)::value, i = n / NC, j = n % NC;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(sum[n & 3][q], sc[i], acc[i][j][q]);
+      asm volatile("" : "+v"(acc[i][j]));  // here and not later, where sums would have to be kept
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    tile_for<0, NR>([&](auto step) __attribute__((always_inline)) {
+      constexpr int i = decltype(step)::value;
+      if constexpr (i + 1 < NR) rv[(i + 1) & 1] = rfrag(rb, i + 1);
+      tile_for<0, PER>([&](auto l) __attribute__((always_inline)) {
+        constexpr int k = i * PER + decltype(l)::value;
+        if constexpr (k < LOADS) issue_one(rn, cn, s + 1, std::integral_constant<int, k>{});
+      });
+      tile_for<0, NC>([&](auto col) __attribute__((always_inline)) {
+        constexpr int j = decltype(col)::value, n = i * NC + j;
+        sum[n & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[j], rv[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f},
+                                                                      0, 0, 0, 0, 0, 0);
+        if constexpr (n >= 2) add(std::integral_constant<int, n - 2>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    add(std::integral_constant<int, NR * NC - 2>{});
+    add(std::integral_constant<int, NR * NC - 1>{});
+  };
+  using First = std::integral_constant<int, 0>;
+  using Second = std::integral_constant<int, 1>;
+
+  if (nst > 0) {
+    // stages go in fours, two for each scale buffer; what is fetched behind the end is zeros
+    fetch_scales(0);
+    tile_for<0, LOADS>([&](auto k) __attribute__((always_inline)) { issue_one(rb0, cb0, 0, k); });
+    store_scales(sb0, 0);
+    auto two = [&](const typename C::Scales& now, typename C::Scales& next, int s) __attribute__((always_inline)) {
+      const float w0 = w_scale(s), w1 = w_scale(s + 1);
+      wait_stage<0>();
+      fetch_scales(s + 2);
+      stage(rb0, cb0, now, rb1, cb1, s, First{}, w0);
+      wait_stage<0>();
+      stage(rb1, cb1, now, rb0, cb0, s + 1, Second{}, w1);
+      store_scales(next, s + 2);
+    };
+    for (int s = 0; s < nst; s += 4) {
+      two(sb0, sb1, s);
+      two(sb1, sb0, s + 2);
+    }
+    wait_stage<0>();  // the last loads into LDS land before it is given back
+  }
+
+  // lane (l16, kq): row l16 of a fragment, columns 8 * (kq >> 1) .. + 7 of column tile
+  // j + (kq & 1) after the exchange
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int q = (wr * NR + i) * 16 + l16;
+    uint16_t* const to = A.out + A.T.row(t.row0 + min(q, t.rows - 1)) * A.ld_out;
+#pragma unroll
+    for (int j = 0; j < NC; j += 2) {
+      using E = Elem<DT>;
+      const f32x4_t a = acc[i][j], b = acc[i][j + 1];
+      const auto lo = __builtin_amdgcn_permlane16_swap(E::pack(a[0], a[1]), E::pack(b[0], b[1]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(E::pack(a[2], a[3]), E::pack(b[2], b[3]), false, false);
+      const int c = c0 + (wc * NC + j + (kq & 1)) * 16 + 8 * (kq >> 1);
+      const uint32_t o[4] = {lo[0], hi[0], lo[1], hi[1]};
+      if (q < t.rows && c < cols) store_words<4>(to + c, o);
+    }
+  }
+}
+
+}  // namespace sgmv_dev
