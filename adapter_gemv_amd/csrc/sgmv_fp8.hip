@@ -181,16 +181,20 @@ __global__ __launch_bounds__(256) void fp8_dequantize_weight_kernel(uint16_t* __
 // ------------------------------------------------------------------------------------
 // products
 // ------------------------------------------------------------------------------------
-template <int DT, bool DX>
+template <int DT, bool DX, bool NEAR>
 hipError_t launch_fp8(hipStream_t s, const Fp8Args& A, const Launch& L) {
   const uint32_t grid = static_cast<uint32_t>(L.workgroups);
-  if (L.rows == 256) fp8_tile_kernel<DT, DX, 256, 256, 2, 4><<<grid, 512, 0, s>>>(A);
-  else fp8_tile_kernel<DT, DX, 128, 128, 2, 2><<<grid, 256, 0, s>>>(A);
+  if (L.rows == 256) fp8_tile_kernel<DT, DX, 256, 256, 2, 4, NEAR><<<grid, 512, 0, s>>>(A);
+  else fp8_tile_kernel<DT, DX, 128, 128, 2, 2, NEAR><<<grid, 256, 0, s>>>(A);
   return hipGetLastError();
 }
 template <bool DX>
 hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const Launch& L) {
-  return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX>(s, A, L) : launch_fp8<SGMV_BF16, DX>(s, A, L);
+  const int32_t depth = DX ? A.h_out : A.h_in;
+  const bool near = depth % 128 == 0 && static_cast<int64_t>(shared_rows(A.T.n, A.share_rows)) * depth <= UINT32_MAX &&
+                    static_cast<int64_t>(A.h_in) * A.h_out <= UINT32_MAX;
+  if (near) return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX, true>(s, A, L) : launch_fp8<SGMV_BF16, DX, true>(s, A, L);
+  return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX, false>(s, A, L) : launch_fp8<SGMV_BF16, DX, false>(s, A, L);
 }
 
 inline Launch fp8_launch(bool dx, int32_t n, int32_t G, bool grouped, int32_t h_in, int32_t h_out) {
@@ -371,6 +375,7 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   Fp8Args A{};
   A.T = {P.starts, P.perm, P.n, P.G};
   A.share = share_of(P.share);
+  A.share_rows = P.share;
   A.r = static_cast<const uint8_t*>(P.r);
   A.r_scale = P.r_scales;
   if (!quantized) {

@@ -34,6 +34,7 @@ struct Fp8Args {
   uint16_t* out;
   int64_t ld_out;
   int32_t h_in, h_out;
+  int32_t share_rows;     // rows that share one of r
 };
 
 __host__ __device__ inline int blocks_of(int h) { return (h + 127) / 128; }
@@ -63,7 +64,10 @@ __device__ inline int swizzle(int k) {
   return B == 256 ? (k & 7) | (k >> 1 & 8) : (k >> 1 & 3) | (k >> 2 & 4);
 }
 
-template <int DT, bool DX, int BR, int BC, int WR, int WC>
+// NEAR: the contracted dimension is a multiple of 128, and an offset into the rows, or into a group of
+// W, fits 32 bits: loads are a uniform base and an offset of the lane's, and need no test (8192^3:
+// see fp8_launch).
+template <int DT, bool DX, int BR, int BC, int WR, int WC, bool NEAR>
 __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
   using C = Fp8Tile<BR, BC, WR, WC>;
   constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI;
@@ -92,38 +96,42 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
     for (int j = 0; j < NC; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
+  const char* const rbase = reinterpret_cast<const char*>(A.r);
   const char* const wbase = reinterpret_cast<const char*>(A.w) + static_cast<int64_t>(t.g) * A.h_in * A.h_out;
   // where this lane's pieces of the first stage are, and how far into the contracted dimension
-  const char *rp[RI], *cp[CI];
+  using Offset = std::conditional_t<NEAR, uint32_t, int64_t>;
+  Offset rp[RI], cp[CI];
   int rk[RI], ck[CI];
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int q = (w * RI + i) * 8 + lane / 8;
     rk[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
     const int j = nst ? A.share.div(A.T.row(t.row0 + min(q, t.rows - 1))) : 0;
-    rp[i] = reinterpret_cast<const char*>(A.r) + static_cast<int64_t>(j) * depth + rk[i];
+    rp[i] = static_cast<Offset>(j) * depth + rk[i];
   }
 #pragma unroll
   for (int i = 0; i < CI; ++i) {
     if constexpr (!DX) {
       const int q = (w * CI + i) * 8 + lane / 8;
       ck[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
-      cp[i] = wbase + static_cast<int64_t>(min(c0 + q, cols - 1)) * A.h_in + ck[i];
+      cp[i] = static_cast<Offset>(min(c0 + q, cols - 1)) * A.h_in + ck[i];
     } else {
       constexpr int L = BC / 16;  // lanes to a contracted row
       ck[i] = (w * CI + i) * (64 / L) + lane / L;
-      cp[i] = wbase + static_cast<int64_t>(ck[i]) * A.h_in + min(c0 + 16 * (lane % L ^ swizzle<BC>(ck[i])), cols - 16);
+      cp[i] = static_cast<Offset>(ck[i]) * A.h_in + min(c0 + 16 * (lane % L ^ swizzle<BC>(ck[i])), cols - 16);
     }
   }
+  // behind the last stage the last one again (NEAR), or zeros
   auto issue_r = [&](typename C::RBuf& to, int s, auto which) __attribute__((always_inline)) {
     constexpr int i = decltype(which)::value;
-    to_lds(rk[i] < depth - s * 128 ? rp[i] + static_cast<int64_t>(s) * 128 : zeros, &to.v[(w * RI + i) * 64]);
+    const char* r = rbase + static_cast<int64_t>(NEAR ? min(s, nst - 1) : s) * 128 + rp[i];
+    to_lds(NEAR || rk[i] < depth - s * 128 ? r : zeros, &to.v[(w * RI + i) * 64]);
   };
   auto issue_c = [&](typename C::CBuf& to, int s, auto which) __attribute__((always_inline)) {
     constexpr int i = decltype(which)::value;
-    const char* c = cp[i] + (DX ? static_cast<int64_t>(s) * 128 * A.h_in : static_cast<int64_t>(s) * 128);
-    if constexpr (DX) asm("" : "+v"(c));  // keeps its computation out of a branch
-    to_lds(ck[i] < depth - s * 128 ? c : zeros, &to.v[(w * CI + i) * 64]);
+    const char* c = wbase + static_cast<int64_t>(NEAR ? min(s, nst - 1) : s) * (DX ? 128 * static_cast<int64_t>(A.h_in) : 128) + cp[i];
+    if constexpr (DX && !NEAR) asm("" : "+v"(c));  // keeps its computation out of a branch
+    to_lds(NEAR || ck[i] < depth - s * 128 ? c : zeros, &to.v[(w * CI + i) * 64]);
   };
   constexpr int LOADS = RI + CI;
   auto issue_one = [&](typename C::RBuf& rt, typename C::CBuf& ct, int s, auto which) __attribute__((always_inline)) {
@@ -134,7 +142,7 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
 
   // Scales.  Of the rows: this thread's row, for one of two stages; fetched two stages ahead, and
   // put into LDS behind the products, in the order in which a lane takes them.  Of the weight: one for
-  // the wavefront's columns (a block's, as they are 64 of a multiple of 64) and stage.  Zero past the end.
+  // the wavefront's columns (a block's, as they are 64 of a multiple of 64) and stage.
   const int sq = tid % BR, ss = tid / BR;
   const int sto = (sq / (16 * NR) * 16 + sq % 16) * NR + sq / 16 % NR;
   const int kb = blocks_of(depth);
@@ -144,11 +152,10 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
   const float* const wp = A.w_scale + static_cast<int64_t>(t.g) * bi * blocks_of(A.h_out) + (DX ? cb : cb * bi);
   float sv = 0.f;
   auto fetch_scales = [&](int s) { sv = global_ptr(sp)[min(s + ss, kb - 1)]; };
-  auto store_scales = [&](typename C::Scales& to, int s) { to.s[ss][sto] = s + ss < nst ? sv : 0.f; };
+  auto store_scales = [&](typename C::Scales& to) { to.s[ss][sto] = sv; };
   auto w_scale = [&](int s) {
-    const int in = min(s, nst - 1);  // no branch: see the tiled product of 16-bit operands
-    const float v = wp[DX ? static_cast<int64_t>(in) * bi : in];
-    return s < nst ? v : 0.f;
+    const int in = min(s, nst - 1);
+    return wp[DX ? static_cast<int64_t>(in) * bi : in];
   };
 
   // Fragment reads: a lane's offsets, made here, plus constants (so that the compiler tells LDS
@@ -185,9 +192,9 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
     }
   };
 
-  // One stage: a step for each row fragment, NC MFMAs; the multiply-adds of an MFMA's sums stand two
-  // MFMAs behind it, the next row fragment is read during a step, and each of the first steps issues a
-  // load or two of the next stage.
+  // One stage: NC MFMAs for each row fragment.  The multiply-adds of an MFMA's sums stand three MFMAs
+  // behind it, when they are there without a wait; the next row fragment is read, and a load or two of
+  // the next stage issued, during each fragment.
   auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb_, const typename C::Scales& sb,
                    typename C::RBuf& rn, typename C::CBuf& cn, int s, auto half, float ws) __attribute__((always_inline)) {
     constexpr int H = decltype(half)::value;
@@ -195,6 +202,9 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
     i32x8_t cv[NC], rv[2];
     f32x4_t sum[4];
     float sc[NR];
+    rv[0] = rfrag(rb, 0);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) cv[j] = cfrag(cb_, j);
     {
       const f32x4_t* const from = reinterpret_cast<const f32x4_t*>(&sb.s[H][(wr * 16 + l16) * NR]);
 #pragma unroll
@@ -204,57 +214,58 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
         for (int q = 0; q < 4; ++q) sc[4 * i + q] = v[q];
       }
     }
-    rv[0] = rfrag(rb, 0);
-#pragma unroll
-    for (int j = 0; j < NC; ++j) cv[j] = cfrag(cb_, j);
-#pragma unroll
-    for (int i = 0; i < NR; ++i) sc[i] *= ws;
     auto add = [&](auto which) __attribute__((always_inline)) {  // the n-th MFMA's sums
       constexpr int n = decltype(which)::value, i = n / NC, j = n % NC;
+      if constexpr (j == 0) sc[i] *= ws;
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(sum[n & 3][q], sc[i], acc[i][j][q]);
       asm volatile("" : "+v"(acc[i][j]));  // here and not later, where sums would have to be kept
     };
     __builtin_amdgcn_sched_barrier(0);
-    tile_for<0, NR>([&](auto step) __attribute__((always_inline)) {
-      constexpr int i = decltype(step)::value;
-      if constexpr (i + 1 < NR) rv[(i + 1) & 1] = rfrag(rb, i + 1);
-      tile_for<0, PER>([&](auto l) __attribute__((always_inline)) {
-        constexpr int k = i * PER + decltype(l)::value;
+    tile_for<0, NR * NC>([&](auto which) __attribute__((always_inline)) {
+      constexpr int n = decltype(which)::value, i = n / NC, j = n % NC;
+      // behind the first MFMA, whose wait for its row fragment would take these reads in
+      if constexpr (j == 1 && i + 1 < NR) rv[(i + 1) & 1] = rfrag(rb, i + 1);
+      if constexpr (j >= 1 && j <= PER) {
+        constexpr int k = i * PER + j - 1;
         if constexpr (k < LOADS) issue_one(rn, cn, s + 1, std::integral_constant<int, k>{});
-      });
-      tile_for<0, NC>([&](auto col) __attribute__((always_inline)) {
-        constexpr int j = decltype(col)::value, n = i * NC + j;
-        sum[n & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[j], rv[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f},
-                                                                      0, 0, 0, 0, 0, 0);
-        if constexpr (n >= 2) add(std::integral_constant<int, n - 2>{});
-      });
+      }
+      sum[n & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[j], rv[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f},
+                                                                    0, 0, 0, 0, 0, 0);
+      if constexpr (n >= 3) add(std::integral_constant<int, n - 3>{});
       __builtin_amdgcn_sched_barrier(0);
     });
-    add(std::integral_constant<int, NR * NC - 2>{});
-    add(std::integral_constant<int, NR * NC - 1>{});
+    tile_for<NR * NC - 3, NR * NC>([&](auto n) __attribute__((always_inline)) { add(n); });
   };
   using First = std::integral_constant<int, 0>;
   using Second = std::integral_constant<int, 1>;
 
   if (nst > 0) {
-    // stages go in fours, two for each scale buffer; what is fetched behind the end is zeros
     fetch_scales(0);
     tile_for<0, LOADS>([&](auto k) __attribute__((always_inline)) { issue_one(rb0, cb0, 0, k); });
-    store_scales(sb0, 0);
-    auto two = [&](const typename C::Scales& now, typename C::Scales& next, int s) __attribute__((always_inline)) {
-      const float w0 = w_scale(s), w1 = w_scale(s + 1);
+    store_scales(sb0);
+    // stage s + k, k of four: two to a scale buffer
+    float wnext = w_scale(0);
+    auto nth = [&](auto which, int s) __attribute__((always_inline)) {
+      constexpr int k = decltype(which)::value;
+      typename C::Scales &now = k < 2 ? sb0 : sb1, &next = k < 2 ? sb1 : sb0;
       wait_stage<0>();
-      fetch_scales(s + 2);
-      stage(rb0, cb0, now, rb1, cb1, s, First{}, w0);
-      wait_stage<0>();
-      stage(rb1, cb1, now, rb0, cb0, s + 1, Second{}, w1);
-      store_scales(next, s + 2);
+      const float ws = wnext;
+      wnext = w_scale(s + k + 1);
+      if constexpr (k % 2 == 0) {
+        fetch_scales(s + k + 2);
+        stage(rb0, cb0, now, rb1, cb1, s + k, First{}, ws);
+      } else {
+        stage(rb1, cb1, now, rb0, cb0, s + k, Second{}, ws);
+        store_scales(next);
+      }
     };
-    for (int s = 0; s < nst; s += 4) {
-      two(sb0, sb1, s);
-      two(sb1, sb0, s + 2);
-    }
+    // no branch inside the loop, which keeps the accumulators where they are
+    int s = 0;
+    for (; s + 4 <= nst; s += 4) tile_for<0, 4>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
+    tile_for<0, 3>([&](auto k) __attribute__((always_inline)) {
+      if (s + decltype(k)::value < nst) nth(k, s);
+    });
     wait_stage<0>();  // the last loads into LDS land before it is given back
   }
 
