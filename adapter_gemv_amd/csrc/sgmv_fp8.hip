@@ -1,6 +1,7 @@
 // 8-bit floating point with a scale for each block of 128: 16-bit values to the format and back,
 // and products with both sides in it.
-#include "sgmv_fp8_tile.h"
+#include "sgmv_fp8_rules.h"
+#include "sgmv_fp8_skinny.h"
 
 using namespace sgmv_dev;
 using namespace sgmv_host;
@@ -8,54 +9,6 @@ using namespace sgmv_host;
 namespace {
 
 constexpr int kBlock = 128;
-
-typedef __attribute__((ext_vector_type(2))) short s16x2_t;
-
-// the larger magnitude of each 16-bit half; magnitudes order like their patterns, infinity and NaN
-// above all
-__device__ inline uint32_t max_halves(uint32_t a, uint32_t b) {
-  typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
-                                                                __builtin_bit_cast(u16x2_t, b)));
-}
-__device__ inline uint32_t top_of(const uint4& v) {
-  constexpr uint32_t kMag = 0x7fff7fffu;
-  const uint32_t t = max_halves(max_halves(v.x & kMag, v.y & kMag), max_halves(v.z & kMag, v.w & kMag));
-  return max(t & 0xffffu, t >> 16);
-}
-
-// The scale of a block whose largest magnitude has the 16 bits `top`: the least power of two,
-// not below 2^-126, whose 448-fold is not below it; NaN for an infinity or a NaN.
-template <int DT>
-__device__ inline float block_scale(uint32_t top) {
-  const float m = Elem<DT>::lo(top);
-  const uint32_t b = __float_as_uint(m);
-  if ((b >> 23) == 255) return __builtin_nanf("");
-  // m = f * 2^p with 1 <= f < 2: 2^(p - 8) if f <= 1.75, 2^(p - 7) above
-  const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
-  return __uint_as_float(static_cast<uint32_t>(max(e, 1)) << 23);
-}
-
-// 8 elements divided by a power of two (or NaN: zeros), as 8 codes
-template <int DT>
-__device__ inline u32x2_t encode8(const uint4& v, float scale) {
-  const bool finite = scale == scale;
-  const float s = finite ? scale : 1.f;
-  s16x2_t c[2] = {};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = word(v, 2 * i), b = word(v, 2 * i + 1);
-    if constexpr (DT == SGMV_BF16) {
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c[i], __builtin_bit_cast(bf16x2_t, a), s, false);
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c[i], __builtin_bit_cast(bf16x2_t, b), s, true);
-    } else {
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(c[i], __builtin_bit_cast(f16x2_t, a), s, false);
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(c[i], __builtin_bit_cast(f16x2_t, b), s, true);
-    }
-  }
-  const u32x2_t o = {__builtin_bit_cast(uint32_t, c[0]), __builtin_bit_cast(uint32_t, c[1])};
-  return finite ? o : u32x2_t{0u, 0u};
-}
 
 // code * scale, rounded once to the 16-bit type: the product has at most 28 bits, which float64
 // holds; what float32 cuts off is kept as its last bit (no later rounding is then misled)
@@ -106,7 +59,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(uint8_t* __restrict__
   const uint4 v = in ? ld16(x + row * R.ld + at) : zero4();
   const float s = block_scale<DT>(block_top(top_of(v)));
   if (!in) return;
-  *reinterpret_cast<u32x2_t*>(codes + row * R.h + at) = encode8<DT>(v, s);
+  *reinterpret_cast<u32x2_t*>(codes + row * R.h + at) = encode8_finite<DT>(v, s);
   if (at % kBlock == 0) scales[row * blocks_of(R.h) + at / kBlock] = s;
 }
 
@@ -154,7 +107,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_weight_kernel(uint8_t* __res
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
     if (c < P.h_in && r < P.h_out)
-      *reinterpret_cast<u32x2_t*>(to + static_cast<int64_t>(r) * P.h_in + c) = encode8<DT>(v[i], s);
+      *reinterpret_cast<u32x2_t*>(to + static_cast<int64_t>(r) * P.h_in + c) = encode8_finite<DT>(v[i], s);
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }
@@ -182,14 +135,17 @@ __global__ __launch_bounds__(256) void fp8_dequantize_weight_kernel(uint16_t* __
 // products
 // ------------------------------------------------------------------------------------
 template <int DT, bool DX, bool NEAR>
-hipError_t launch_fp8(hipStream_t s, const Fp8Args& A, const Launch& L) {
+hipError_t launch_fp8(hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
   const uint32_t grid = static_cast<uint32_t>(L.workgroups);
-  if (L.rows == 256) fp8_tile_kernel<DT, DX, 256, 256, 2, 4, NEAR><<<grid, 512, 0, s>>>(A);
-  else fp8_tile_kernel<DT, DX, 128, 128, 2, 2, NEAR><<<grid, 256, 0, s>>>(A);
+  if (L.rows == 256) fp8_tile_kernel<DT, DX, 256, 256, 2, 4, 2, NEAR><<<grid, 512, 0, s>>>(A);
+  else if (L.rows == 64 && L.buffers == 8) fp8_tile_kernel<DT, DX, 64, 64, 2, 2, 8, NEAR><<<grid, 256, 0, s>>>(A);
+  else if (L.rows == 64) fp8_tile_kernel<DT, DX, 64, 64, 2, 2, 4, NEAR><<<grid, 256, 0, s>>>(A);
+  else if (L.buffers == 4) fp8_tile_kernel<DT, DX, 128, 128, 2, 2, 4, NEAR><<<grid, 256, 0, s>>>(A);
+  else fp8_tile_kernel<DT, DX, 128, 128, 2, 2, 2, NEAR><<<grid, 256, 0, s>>>(A);
   return hipGetLastError();
 }
 template <bool DX>
-hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const Launch& L) {
+hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
   const int32_t depth = DX ? A.h_out : A.h_in;
   const bool near = depth % 128 == 0 && static_cast<int64_t>(shared_rows(A.T.n, A.share_rows)) * depth <= UINT32_MAX &&
                     static_cast<int64_t>(A.h_in) * A.h_out <= UINT32_MAX;
@@ -197,15 +153,16 @@ hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const Laun
   return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX, false>(s, A, L) : launch_fp8<SGMV_BF16, DX, false>(s, A, L);
 }
 
-inline Launch fp8_launch(bool dx, int32_t n, int32_t G, bool grouped, int32_t h_in, int32_t h_out) {
-  const int32_t out = dx ? h_in : h_out;
-  const auto expected = [&](int B) {
-    const double rows = n;
-    return (grouped ? rows / B + 0.5 * std::min(n, G) : std::ceil(rows / B)) * tiles_of(out, B);
-  };
-  const int B = big_tiles(expected(256), expected(128)) ? 256 : 128;
-  const int64_t tiles = max_row_tiles(n, G, grouped, B) * tiles_of(out, B);
-  return {B, B, B == 256 ? 8 : 4, tiles_of(tiles, kTileXcds) * kTileXcds};
+template <int DT, bool X16>
+hipError_t launch_fp8_skinny(hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
+  const uint32_t grid = static_cast<uint32_t>(L.workgroups);
+  if (L.cols == 16) fp8_skinny_kernel<DT, X16, 1, 8><<<grid, 512, 0, s>>>(A);
+  else fp8_skinny_kernel<DT, X16, 2, 4><<<grid, 256, 0, s>>>(A);
+  return hipGetLastError();
+}
+hipError_t launch_fp8_skinny(int32_t dtype, hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
+  if (A.x) return dtype == SGMV_F16 ? launch_fp8_skinny<SGMV_F16, true>(s, A, L) : launch_fp8_skinny<SGMV_BF16, true>(s, A, L);
+  return dtype == SGMV_F16 ? launch_fp8_skinny<SGMV_F16, false>(s, A, L) : launch_fp8_skinny<SGMV_BF16, false>(s, A, L);
 }
 
 // ------------------------------------------------------------------------------------
@@ -347,13 +304,14 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
       (st = check_fp8_dim(P.h_out)) || (st = check_dim(P.cols(), P.ld_out)))
     return st;
   if (!quantized && (st = check_fp8_rows(P.dtype, P.rows(), P.depth(), P.ld_r))) return st;
-  const Launch L = fp8_launch(P.dx, P.n, P.G, P.starts, P.h_in, P.h_out);
+  const BlockLaunch L = fp8_launch(P.dx, P.n, P.G, P.starts, P.h_in, P.h_out);
   if (!L.fits()) return SGMV_ERR_SHAPE;
   if (P.n == 0) return SGMV_OK;
   if (!P.out || !P.r || (quantized && !P.r_scales) || !P.w || !P.w_scales) return SGMV_ERR_NULL;
   if (!aligned16(P.out) || !aligned16(P.r) || !aligned4(P.r_scales) || !aligned16(P.w) || !aligned4(P.w_scales))
     return SGMV_ERR_ALIGNMENT;
-  const size_t room = quantized ? 0 : rows_room(P.rows(), P.depth());
+  const bool few = L.rows == kSkinnyRows;
+  const size_t room = quantized || few ? 0 : rows_room(P.rows(), P.depth());
   if (room > 0 && (!P.workspace || P.workspace_bytes < room || !aligned16(P.workspace))) return SGMV_ERR_WORKSPACE;
   const size_t out_bytes = matrix_bytes(P.n, P.ld_out, P.cols()), elems = static_cast<size_t>(P.G) * P.h_in * P.h_out;
   const struct {
@@ -376,9 +334,13 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   A.T = {P.starts, P.perm, P.n, P.G};
   A.share = share_of(P.share);
   A.share_rows = P.share;
-  A.r = static_cast<const uint8_t*>(P.r);
-  A.r_scale = P.r_scales;
-  if (!quantized) {
+  if (quantized) {
+    A.r = static_cast<const uint8_t*>(P.r);
+    A.r_scale = P.r_scales;
+  } else if (few) {
+    A.x = static_cast<const uint16_t*>(P.r);
+    A.ld_x = P.ld_r;
+  } else {
     uint8_t* const codes = static_cast<uint8_t*>(P.workspace);
     float* const scales = reinterpret_cast<float*>(codes + codes_room(P.rows(), P.depth()));
     if (hipError_t e = launch_quantize(P.dtype, stream, codes, scales, P.r, fp8_rows(P.rows(), P.depth(), P.ld_r)))
@@ -389,6 +351,7 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   A.w_scale = P.w_scales;
   A.out = static_cast<uint16_t*>(P.out);
   A.ld_out = P.ld_out, A.h_in = P.h_in, A.h_out = P.h_out;
+  if (few) return hip_status(launch_fp8_skinny(P.dtype, stream, A, L));
   return hip_status(P.dx ? launch_fp8<true>(P.dtype, stream, A, L) : launch_fp8<false>(P.dtype, stream, A, L));
 }
 
@@ -396,7 +359,8 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
 
 extern "C" size_t sgmv_block_workspace_bytes(int32_t n, int32_t share, int32_t n_groups, int32_t grouped, int32_t h_in,
                                            int32_t h_out) {
-  if (n < 1 || share < 1 || h_in < 1) return 0;
+  if (n < 1 || share < 1 || n_groups < 1 || h_in < 1 || h_out < 1) return 0;
+  if (fp8_launch(false, n, n_groups, grouped != 0, h_in, h_out).rows == kSkinnyRows) return 0;
   return rows_room(shared_rows(n, share), h_in);
 }
 

@@ -2,8 +2,8 @@
 // W^T, or rows of dy times W (DX).
 //
 // A workgroup makes BR rows x BC columns of the output; a stage is one block of the contracted
-// dimension, 128 bytes of each row and column, brought by direct global-to-LDS loads into one of two
-// buffers while the other is multiplied.  An MFMA 16x16x128 takes a whole block; its sums start from
+// dimension, 128 bytes of each row and column, brought by direct global-to-LDS loads into one of
+// BUFS buffers while another is multiplied.  An MFMA 16x16x128 takes a whole block; its sums start from
 // zero and are added to the tile's, times the block's two scales: 128 multiply-adds for 32 matrix
 // instructions of a wavefront, which run beside them.
 //
@@ -27,53 +27,71 @@ typedef __attribute__((ext_vector_type(2))) int i32x2_t;
 struct Fp8Args {
   RowTab T;
   Share share;
+  const uint16_t* x;      // rows in 16 bits, ld_x elements apart, or
   const uint8_t* r;       // rows of x or dy, dense
   const float* r_scale;   // [rows, blocks]
   const uint8_t* w;       // [h_out, h_in]
   const float* w_scale;   // [blocks of h_out, blocks of h_in]
   uint16_t* out;
-  int64_t ld_out;
+  int64_t ld_x, ld_out;
   int32_t h_in, h_out;
   int32_t share_rows;     // rows that share one of r
 };
 
 __host__ __device__ inline int blocks_of(int h) { return (h + 127) / 128; }
 
-template <int BR, int BC, int WR, int WC>
+template <int BR, int BC, int WR, int WC, int BUFS>
 struct Fp8Tile {
   static constexpr int NW = WR * WC, TH = 64 * NW;
   static constexpr int NR = BR / WR / 16, NC = BC / WC / 16;  // fragments of a wavefront
   static constexpr int RI = BR / 8 / NW, CI = BC / 8 / NW;    // loads per stage
-  static_assert(RI * 8 * NW == BR && CI * 8 * NW == BC && NC == 4 && NR % 4 == 0 && RI + CI <= NR * 2, "");
-  static_assert(TH == 2 * BR, "a thread fetches a row's scale of one of two stages");
+  static_assert(RI * 8 * NW == BR && CI * 8 * NW == BC && NC % 2 == 0 && NC <= 4 && NR * NC >= 4, "");
+  static_assert(BR < TH && BR % 64 == 0, "a wavefront to 64 rows' scales, and one to the weight's");
   struct RBuf {
     u32x4_t v[BR * 8];
   };
   struct CBuf {
     u32x4_t v[BC * 8];
   };
+  static constexpr int CB = (BC + 127) / 128;  // blocks of columns
   struct Scales {
-    alignas(16) float s[2][BR];  // [stage of two][wavefront rows][row of 16][fragment]
+    alignas(16) float r[BR];  // [wavefront rows][row of 16][fragment]
+    float w[64];              // of the blocks of columns, in turn
   };
 };
+
+// at most N global loads of this wavefront are in flight, and every LDS access of it is done; then the
+// workgroup's barrier
+template <int N>
+__device__ inline void wait_tile() {
+  static_assert(N < 64, "vmcnt range");
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// the I-th buffer of its type in a kernel
+template <class B, int I>
+__device__ __forceinline__ B& stage_buffer() {
+  __shared__ B b;
+  return b;
+}
 
 // DX, tiles of B columns: where a piece of contracted row k is moved
 template <int B>
 __device__ inline int swizzle(int k) {
-  static_assert(B == 256 || B == 128, "");
-  return B == 256 ? (k & 7) | (k >> 1 & 8) : (k >> 1 & 3) | (k >> 2 & 4);
+  static_assert(B == 256 || B == 128 || B == 64, "");
+  return B == 256 ? (k & 7) | (k >> 1 & 8) : B == 128 ? (k >> 1 & 3) | (k >> 2 & 4) : (k >> 2 & 1) | (k >> 3 & 2);
 }
 
 // NEAR: the contracted dimension is a multiple of 128, and an offset into the rows, or into a group of
 // W, fits 32 bits: loads are a uniform base and an offset of the lane's, and need no test (8192^3:
 // see fp8_launch).
-template <int DT, bool DX, int BR, int BC, int WR, int WC, bool NEAR>
-__global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
-  using C = Fp8Tile<BR, BC, WR, WC>;
-  constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI;
-  __shared__ typename C::RBuf rb0, rb1;
-  __shared__ typename C::CBuf cb0, cb1;
-  __shared__ typename C::Scales sb0, sb1;
+template <int DT, bool DX, int BR, int BC, int WR, int WC, int BUFS, bool NEAR>
+__global__ __launch_bounds__(64 * WR * WC, BUFS * BR >= 512 && BR < 256 ? 1 : 2) void fp8_tile_kernel(Fp8Args A) {
+  using C = Fp8Tile<BR, BC, WR, WC, BUFS>;
+  constexpr int NR = C::NR, NC = C::NC, RI = C::RI, CI = C::CI, CB = C::CB;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, kq = lane >> 4;
   const int wr = w / WC, wc = w % WC;
   const int cols = DX ? A.h_in : A.h_out, depth = DX ? A.h_out : A.h_in, bi = blocks_of(A.h_in);
@@ -140,22 +158,24 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
     else issue_c(ct, s, std::integral_constant<int, k - RI>{});
   };
 
-  // Scales.  Of the rows: this thread's row, for one of two stages; fetched two stages ahead, and
-  // put into LDS behind the products, in the order in which a lane takes them.  Of the weight: one for
-  // the wavefront's columns (a block's, as they are 64 of a multiple of 64) and stage.
-  const int sq = tid % BR, ss = tid / BR;
-  const int sto = (sq / (16 * NR) * 16 + sq % 16) * NR + sq / 16 % NR;
+  // Scales come the same way, 4 bytes to a lane: the first wavefronts fetch the rows', in the order in
+  // which a lane takes them, and the others the weight's.
   const int kb = blocks_of(depth);
   const float* sp = A.r_scale;
-  if (nst) sp += static_cast<int64_t>(A.share.div(A.T.row(t.row0 + min(sq, t.rows - 1)))) * kb;
-  const int cb = min(c0 + wc * 16 * NC, cols - 1) / 128;
-  const float* const wp = A.w_scale + static_cast<int64_t>(t.g) * bi * blocks_of(A.h_out) + (DX ? cb : cb * bi);
-  float sv = 0.f;
-  auto fetch_scales = [&](int s) { sv = global_ptr(sp)[min(s + ss, kb - 1)]; };
-  auto store_scales = [&](typename C::Scales& to) { to.s[ss][sto] = sv; };
-  auto w_scale = [&](int s) {
-    const int in = min(s, nst - 1);
-    return wp[DX ? static_cast<int64_t>(in) * bi : in];
+  int64_t step = 1;
+  if (nst) {
+    if (tid < BR) {
+      const int q = (tid / (16 * NR) * NR + tid % NR) * 16 + tid / NR % 16;
+      sp += static_cast<int64_t>(A.share.div(A.T.row(t.row0 + min(q, t.rows - 1)))) * kb;
+    } else {
+      const int cb = min(c0 + 128 * (lane % CB), cols - 1) / 128;
+      sp = A.w_scale + static_cast<int64_t>(t.g) * bi * blocks_of(A.h_out) + (DX ? cb : cb * bi);
+      if (DX) step = bi;
+    }
+  }
+  auto issue_s = [&](typename C::Scales& to, int s) __attribute__((always_inline)) {
+    float* const at = w * 64 < BR ? to.r + w * 64 : to.w;
+    __builtin_amdgcn_global_load_lds((tile_global_void*)(sp + min(s, nst - 1) * step), (tile_lds_void*)at, 4, 0, 0);
   };
 
   // Fragment reads: a lane's offsets, made here, plus constants (so that the compiler tells LDS
@@ -196,9 +216,8 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
   // behind it, when they are there without a wait; the next row fragment is read, and a load or two of
   // the next stage issued, during each fragment.
   auto stage = [&](const typename C::RBuf& rb, const typename C::CBuf& cb_, const typename C::Scales& sb,
-                   typename C::RBuf& rn, typename C::CBuf& cn, int s, auto half, float ws) __attribute__((always_inline)) {
-    constexpr int H = decltype(half)::value;
-    constexpr int PER = (LOADS + NR - 1) / NR;
+                   typename C::RBuf& rn, typename C::CBuf& cn, typename C::Scales& sn, int s) __attribute__((always_inline)) {
+    constexpr int LAST = NR * NC;
     i32x8_t cv[NC], rv[2];
     f32x4_t sum[4];
     float sc[NR];
@@ -206,14 +225,17 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
 #pragma unroll
     for (int j = 0; j < NC; ++j) cv[j] = cfrag(cb_, j);
     {
-      const f32x4_t* const from = reinterpret_cast<const f32x4_t*>(&sb.s[H][(wr * 16 + l16) * NR]);
+      constexpr int W = NR < 4 ? NR : 4;
+      typedef __attribute__((ext_vector_type(W))) float part_t;
+      const part_t* const from = reinterpret_cast<const part_t*>(&sb.r[(wr * 16 + l16) * NR]);
 #pragma unroll
-      for (int i = 0; i < NR / 4; ++i) {
-        const f32x4_t v = from[i];
+      for (int i = 0; i < NR / W; ++i) {
+        const part_t v = from[i];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sc[4 * i + q] = v[q];
+        for (int q = 0; q < W; ++q) sc[W * i + q] = v[q];
       }
     }
+    const float ws = sb.w[wc * 16 * NC / 128];
     auto add = [&](auto which) __attribute__((always_inline)) {  // the n-th MFMA's sums
       constexpr int n = decltype(which)::value, i = n / NC, j = n % NC;
       if constexpr (j == 0) sc[i] *= ws;
@@ -222,51 +244,51 @@ __global__ __launch_bounds__(64 * WR * WC, 2) void fp8_tile_kernel(Fp8Args A) {
       asm volatile("" : "+v"(acc[i][j]));  // here and not later, where sums would have to be kept
     };
     __builtin_amdgcn_sched_barrier(0);
-    tile_for<0, NR * NC>([&](auto which) __attribute__((always_inline)) {
+    tile_for<0, LAST>([&](auto which) __attribute__((always_inline)) {
       constexpr int n = decltype(which)::value, i = n / NC, j = n % NC;
       // behind the first MFMA, whose wait for its row fragment would take these reads in
       if constexpr (j == 1 && i + 1 < NR) rv[(i + 1) & 1] = rfrag(rb, i + 1);
-      if constexpr (j >= 1 && j <= PER) {
-        constexpr int k = i * PER + j - 1;
-        if constexpr (k < LOADS) issue_one(rn, cn, s + 1, std::integral_constant<int, k>{});
-      }
+      tile_for<0, LOADS>([&](auto l) __attribute__((always_inline)) {
+        if constexpr (1 + decltype(l)::value * (LAST - 1) / LOADS == n) issue_one(rn, cn, s + BUFS - 1, l);
+      });
+      if constexpr (n == 2) issue_s(sn, s + BUFS - 1);
       sum[n & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[j], rv[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f},
                                                                     0, 0, 0, 0, 0, 0);
       if constexpr (n >= 3) add(std::integral_constant<int, n - 3>{});
       __builtin_amdgcn_sched_barrier(0);
     });
-    tile_for<NR * NC - 3, NR * NC>([&](auto n) __attribute__((always_inline)) { add(n); });
+    tile_for<LAST - 3, LAST>([&](auto n) __attribute__((always_inline)) { add(n); });
   };
-  using First = std::integral_constant<int, 0>;
-  using Second = std::integral_constant<int, 1>;
-
+  // Buffers by number; each is an object of its own, by which the compiler tells them apart
+  auto rbuf = [&](auto k) __attribute__((always_inline)) -> typename C::RBuf& {
+    return stage_buffer<typename C::RBuf, decltype(k)::value % BUFS>();
+  };
+  auto cbuf = [&](auto k) __attribute__((always_inline)) -> typename C::CBuf& {
+    return stage_buffer<typename C::CBuf, decltype(k)::value % BUFS>();
+  };
+  auto sbuf = [&](auto k) __attribute__((always_inline)) -> typename C::Scales& {
+    return stage_buffer<typename C::Scales, decltype(k)::value % BUFS>();
+  };
   if (nst > 0) {
-    fetch_scales(0);
-    tile_for<0, LOADS>([&](auto k) __attribute__((always_inline)) { issue_one(rb0, cb0, 0, k); });
-    store_scales(sb0);
-    // stage s + k, k of four: two to a scale buffer
-    float wnext = w_scale(0);
+    tile_for<0, BUFS - 1>([&](auto k) __attribute__((always_inline)) {
+      tile_for<0, LOADS>([&](auto l) __attribute__((always_inline)) { issue_one(rbuf(k), cbuf(k), decltype(k)::value, l); });
+      issue_s(sbuf(k), decltype(k)::value);
+    });
+    // stage s + k, k of a round.  The buffer that it fills is the one that the stage before read.
+    constexpr int ROUND = BUFS > 4 ? BUFS : 4;
     auto nth = [&](auto which, int s) __attribute__((always_inline)) {
       constexpr int k = decltype(which)::value;
-      typename C::Scales &now = k < 2 ? sb0 : sb1, &next = k < 2 ? sb1 : sb0;
-      wait_stage<0>();
-      const float ws = wnext;
-      wnext = w_scale(s + k + 1);
-      if constexpr (k % 2 == 0) {
-        fetch_scales(s + k + 2);
-        stage(rb0, cb0, now, rb1, cb1, s + k, First{}, ws);
-      } else {
-        stage(rb1, cb1, now, rb0, cb0, s + k, Second{}, ws);
-        store_scales(next);
-      }
+      using Fill = std::integral_constant<int, k + BUFS - 1>;
+      wait_tile<(BUFS - 2) * (LOADS + 1)>();
+      stage(rbuf(which), cbuf(which), sbuf(which), rbuf(Fill{}), cbuf(Fill{}), sbuf(Fill{}), s + k);
     };
     // no branch inside the loop, which keeps the accumulators where they are
     int s = 0;
-    for (; s + 4 <= nst; s += 4) tile_for<0, 4>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
-    tile_for<0, 3>([&](auto k) __attribute__((always_inline)) {
+    for (; s + ROUND <= nst; s += ROUND) tile_for<0, ROUND>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
+    tile_for<0, ROUND - 1>([&](auto k) __attribute__((always_inline)) {
       if (s + decltype(k)::value < nst) nth(k, s);
     });
-    wait_stage<0>();  // the last loads into LDS land before it is given back
+    wait_tile<0>();  // the last loads into LDS land before it is given back
   }
 
   // lane (l16, kq): row l16 of a fragment, columns 8 * (kq >> 1) .. + 7 of column tile

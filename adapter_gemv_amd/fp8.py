@@ -27,11 +27,26 @@ def _blocks(h: int) -> int:
     return (h + BLOCK - 1) // BLOCK
 
 
+def _empty(like, shape, dtype, stream):
+    """An allocation on ``like``'s device for work on ``stream``."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _made(kind, codes, scales):
+    """A value of parts that need no check."""
+    q = object.__new__(kind)
+    q.codes, q.scales = codes, scales
+    return q
+
+
 def _check_parts(codes, scales, shape):
     torch = _torch()
-    if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.float32:
+    if codes.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32:
         raise TypeError("codes must be float8_e4m3fn and scales float32")
-    if tuple(scales.shape) != shape:
+    if scales.shape != shape:
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not match: "
                          f"scales must be {shape}")
     if not codes.is_contiguous() or not scales.is_contiguous():
@@ -48,7 +63,8 @@ class Fp8Rows:
         c = self.codes
         if c.dim() < 1:
             raise ValueError("codes must be [.., h]")
-        _check_parts(c, self.scales, (*c.shape[:-1], _blocks(c.shape[-1])))
+        s = c.shape
+        _check_parts(c, self.scales, (*s[:-1], _blocks(s[-1])))
 
     @property
     def shape(self):
@@ -67,7 +83,8 @@ class Fp8Weight:
         c = self.codes
         if c.dim() not in (2, 3):
             raise ValueError("codes must be [E, h_out, h_in] or [h_out, h_in]")
-        _check_parts(c, self.scales, (*c.shape[:-2], _blocks(c.shape[-2]), _blocks(c.shape[-1])))
+        s = c.shape
+        _check_parts(c, self.scales, (*s[:-2], _blocks(s[-2]), _blocks(s[-1])))
 
     @property
     def shape(self):
@@ -93,13 +110,11 @@ def fp8_quantize(x, stream=None) -> Fp8Rows:
     check_sizes("sgmv_block_quantize", h)
     dt = dtype_code(x)
     handle = _stream_of(stream, x)
-    lead = tuple(x.shape)[:-1]
-    with _on(stream):
-        codes = x.new_empty((*lead, h), dtype=torch.float8_e4m3fn)
-        scales = x.new_empty((*lead, _blocks(h)), dtype=torch.float32)
+    codes = _empty(x, x.shape, torch.float8_e4m3fn, stream)
+    scales = _empty(x, (*x.shape[:-1], _blocks(h)), torch.float32, stream)
     st = _lib.lib().sgmv_block_quantize(handle, dt, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), ld, rows, h)
     check(st, "sgmv_block_quantize")
-    return Fp8Rows(codes, scales)
+    return _made(Fp8Rows, codes, scales)
 
 
 def fp8_quantize_weight(W, stream=None) -> Fp8Weight:
@@ -110,14 +125,12 @@ def fp8_quantize_weight(W, stream=None) -> Fp8Weight:
     check_sizes("sgmv_block_quantize_weight", E, h_out, h_in)
     dt = dtype_code(W)
     handle = _stream_of(stream, W)
-    lead = tuple(W.shape)[:-2]
-    with _on(stream):
-        codes = W.new_empty(tuple(W.shape), dtype=torch.float8_e4m3fn)
-        scales = W.new_empty((*lead, _blocks(h_out), _blocks(h_in)), dtype=torch.float32)
+    codes = _empty(W, W.shape, torch.float8_e4m3fn, stream)
+    scales = _empty(W, (*W.shape[:-2], _blocks(h_out), _blocks(h_in)), torch.float32, stream)
     st = _lib.lib().sgmv_block_quantize_weight(handle, dt, codes.data_ptr(), scales.data_ptr(), W.data_ptr(), stride,
                                              E, h_in, h_out)
     check(st, "sgmv_block_quantize_weight")
-    return Fp8Weight(codes, scales)
+    return _made(Fp8Weight, codes, scales)
 
 
 def fp8_dequantize(y, q, stream=None):
@@ -144,29 +157,31 @@ def fp8_dequantize(y, q, stream=None):
 
 
 def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: bool):
-    torch = _torch()
     where = "sgmv_block_matmul_dx" if dx else "sgmv_block_matmul"
-    n = int(out.shape[0])
+    n = out.shape[0]
     _check_rows(out, n, "dx" if dx else "y")
     E = 1 if groups is None else groups.n_groups
-    shape = W.shape if len(W.shape) == 3 else (1, *W.shape)
-    if shape[0] != E:
+    codes, scales = W.codes, W.scales
+    shape = codes.shape
+    h_out, h_in = shape[-2:]
+    if (shape[0] if len(shape) == 3 else 1) != E:
         raise ValueError(f"W must be [{E}, h_out, h_in]")
-    _, h_out, h_in = shape
     depth, cols = (h_out, h_in) if dx else (h_in, h_out)
-    rs = tuple(rows.shape)
+    eight = isinstance(rows, Fp8Rows)
+    rs = rows.shape
     if len(rs) != 2 or rs[1] != depth or out.shape[1] != cols:
-        raise ValueError(f"rows {rs} and output {tuple(out.shape)} do not match W's h_in = {h_in}, h_out = {h_out}")
+        raise ValueError(f"rows {tuple(rs)} and output {tuple(out.shape)} do not match W's h_in = {h_in}, "
+                         f"h_out = {h_out}")
     if dx and rs[0] != n:
         raise ValueError(f"dy has {rs[0]} rows, dx {n}")
     check_sizes(where, n, h_in, h_out)
     dt, share = dtype_code(out), _share(n, rs[0])
     starts, perm, E = _tables(groups, n, out)
     lib = _lib.lib()
-    if isinstance(rows, Fp8Rows):
-        handle = _stream_of(stream, out, rows.codes, rows.scales, W.codes, W.scales)
+    tail = (codes.data_ptr(), scales.data_ptr(), starts, perm, n, E, h_in, h_out)
+    if eight:
+        handle = _stream_of(stream, out, rows.codes, rows.scales, codes, scales)
         head = (handle, dt, out.data_ptr(), _ld(out), rows.codes.data_ptr(), rows.scales.data_ptr())
-        tail = (W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, E, h_in, h_out)
         st = (lib.sgmv_block_matmul_dx_quantized(*head, *tail) if dx else
               lib.sgmv_block_matmul_quantized(*head, share, *tail))
         check(st, where + "_quantized")
@@ -174,17 +189,16 @@ def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: b
     _check_rows(rows, rs[0], "dy" if dx else "x")
     if rows.dtype != out.dtype:
         raise TypeError("the rows and the output must share a dtype")
-    handle = _stream_of(stream, out, rows, W.codes, W.scales)
+    handle = _stream_of(stream, out, rows, codes, scales)
     room = (lib.sgmv_block_dx_workspace_bytes(n, h_out) if dx else
             lib.sgmv_block_workspace_bytes(n, share, E, starts is not None, h_in, h_out))
     at = None
     if room:
-        with _on(stream):
-            space = out.new_empty(room, dtype=torch.uint8)
+        space = _empty(out, room, _torch().uint8, stream)
         at = space.data_ptr()
     head = (handle, dt, out.data_ptr(), _ld(out), rows.data_ptr(), _ld(rows))
-    tail = (W.codes.data_ptr(), W.scales.data_ptr(), starts, perm, n, E, h_in, h_out, at, room)
-    st = lib.sgmv_block_matmul_dx(*head, *tail) if dx else lib.sgmv_block_matmul(*head, share, *tail)
+    st = (lib.sgmv_block_matmul_dx(*head, *tail, at, room) if dx else
+          lib.sgmv_block_matmul(*head, share, *tail, at, room))
     check(st, where)
     return out
 
