@@ -1,5 +1,7 @@
 // Routing to experts and its gradient, and the weighted sum of each token's expert rows and its
 // gradients.
+#include <type_traits>
+
 #include "sgmv_device.h"
 #include "sgmv_rules.h"
 
@@ -35,18 +37,51 @@ __device__ inline void store_logit(void* p, int64_t i, float v) {
   else static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(Elem<DT>::pack(v, 0.f));
 }
 
-__device__ inline double wave_sum(double v) {
-  for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
+// Reductions over the L lanes of a token (16: a row of the wavefront, by rotations within it), in every
+// lane; all of them have to take part.
+template <typename T>
+__device__ inline T from_lane(T v, int lane) { return __shfl(v, lane); }
+template <int CTRL>
+__device__ inline uint32_t rotated(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 15, 15, false));
+}
+template <int L, typename T, typename F>
+__device__ inline T over_token(T v, F op) {
+  static_assert(L == 16 || L == 64, "");
+  if constexpr (sizeof(T) == 4) {
+    constexpr int kRotate = 0x120;  // row_ror
+    const auto turn = [](T x, auto by) {
+      return __builtin_bit_cast(T, rotated<kRotate + decltype(by)::value>(__builtin_bit_cast(uint32_t, x)));
+    };
+    v = op(v, turn(v, std::integral_constant<int, 8>{}));
+    v = op(v, turn(v, std::integral_constant<int, 4>{}));
+    v = op(v, turn(v, std::integral_constant<int, 2>{}));
+    v = op(v, turn(v, std::integral_constant<int, 1>{}));
+  } else {
+#pragma unroll
+    for (int d = 8; d; d /= 2) v = op(v, __shfl_xor(v, d));
+  }
+  if constexpr (L == 64) {
+    v = op(v, __shfl_xor(v, 16));
+    v = op(v, __shfl_xor(v, 32));
+  }
   return v;
 }
-__device__ inline float wave_sum(float v) {
-  for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
-  return v;
+template <int L, typename T>
+__device__ inline T token_sum(T v) {
+  return over_token<L>(v, [](T a, T b) { return a + b; });
 }
-__device__ inline float wave_max(float v) {
-  for (int d = 32; d; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+template <int L>
+__device__ inline float token_max(float v) {
+  return over_token<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
+template <int L>
+__device__ inline bool token_any(bool v) {
+  const uint64_t set = __ballot(v);
+  return L == 64 ? set != 0 : (set >> (threadIdx.x & 48) & 0xffffu) != 0;
+}
+
+constexpr float kInf = __builtin_inff();
 
 // an unsigned number that orders like the value, NaN above all; 0 stands for "not there"
 __device__ inline uint64_t order(double v) {
@@ -54,51 +89,57 @@ __device__ inline uint64_t order(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 counts as 0
   return b >> 63 ? ~b : b | uint64_t(1) << 63;
 }
+// the same for a value that is no NaN; 0 for minus infinity
+__device__ inline uint32_t order(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return v == -kInf ? 0u : b >> 31 ? ~b : b | 0x80000000u;
+}
 
 // s_j over the sum of the chosen s, times a common factor that keeps the largest near 1: `top` is
-// the largest chosen logit
+// the largest chosen logit (a sigmoid by itself: 0)
 template <bool SIGMOID, typename T>
 __device__ inline T share_of_choice(T l, T top) {
   if constexpr (!SIGMOID) return exp(l - top);
   else return l >= 0 ? 1 / (1 + exp(-l)) : exp(l - (top < 0 ? top : T(0))) / (1 + exp(l));
 }
 
-// One wavefront to a token.  c in 64 bits: of the values that choose, a row's neighbours are
-// often closer than float32's rounding.
-template <int DT, bool SIGMOID>
-__global__ __launch_bounds__(64) void route_kernel(RouteArgs A, bool normalize) {
-  __shared__ uint64_t key[kMaxGroups];  // order of c; 0: not to be chosen
-  __shared__ double val[kMaxGroups];
-  __shared__ uint64_t group_key[kMaxExpertGroups];
-  const int lane = threadIdx.x, t = blockIdx.x;
+// One token by the whole wavefront, with the values that choose in 64 bits: for tokens whose choice
+// float32 leaves open, and for NaN.
+template <int N>
+struct ExactSpace {
+  uint64_t key[N];  // order of c; 0: not to be chosen
+  double val[N];
+  uint64_t group_key[kMaxExpertGroups];
+};
+template <int DT, bool SIGMOID, int N>
+__device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, ExactSpace<N>& S) {
+  const int lane = threadIdx.x;
   const int64_t at = t * A.ld;
-  float top = -__builtin_inff();
+  float top = -kInf;
   bool bad = false;
   for (int e = lane; e < A.E; e += 64) {
     const float l = logit<DT>(A.logits, at + e);
-    bad |= !(l < __builtin_inff());
+    bad |= !(l < kInf);
     top = fmaxf(top, l);
   }
   bad = __any(bad);
-  top = wave_max(top);
+  top = token_max<64>(top);
   double sum = 0;
   if (!SIGMOID) {
     for (int e = lane; e < A.E; e += 64) sum += exp(static_cast<double>(logit<DT>(A.logits, at + e)) - top);
-    sum = wave_sum(sum);
+    sum = token_sum<64>(sum);
   }
   auto score = [&](float l) -> double {
     if (SIGMOID) return 1 / (1 + exp(-static_cast<double>(l)));
     return bad ? __builtin_nan("") : exp(static_cast<double>(l) - top) / sum;
   };
-  // scores grow with logits, so these choose as well where nothing is added to a score
   const bool by_logit = !A.bias && (A.keep == A.groups || A.best == 1);
   for (int e = lane; e < A.E; e += 64) {
     const float l = logit<DT>(A.logits, at + e);
     const double c = by_logit ? (!SIGMOID && bad ? __builtin_nan("") : static_cast<double>(l))
                               : score(l) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0);
-    const bool out = l == -__builtin_inff() || c == -__builtin_inf();
-    key[e] = out ? 0 : order(c);
-    val[e] = c;
+    S.key[e] = l == -kInf || c == -__builtin_inf() ? 0 : order(c);
+    S.val[e] = c;
   }
   __syncthreads();
   if (A.keep < A.groups) {
@@ -106,19 +147,19 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, bool normalize) 
     if (lane < A.groups) {
       int b0 = -1, b1 = -1;
       for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        if (key[e] == 0) continue;
-        if (b0 < 0 || key[e] > key[b0]) b1 = b0, b0 = e;
-        else if (b1 < 0 || key[e] > key[b1]) b1 = e;
+        if (S.key[e] == 0) continue;
+        if (b0 < 0 || S.key[e] > S.key[b0]) b1 = b0, b0 = e;
+        else if (b1 < 0 || S.key[e] > S.key[b1]) b1 = e;
       }
-      group_key[lane] = b0 < 0 ? 0 : order(val[b0] + (A.best > 1 && b1 >= 0 ? val[b1] : 0.0));
+      S.group_key[lane] = b0 < 0 ? 0 : order(S.val[b0] + (A.best > 1 && b1 >= 0 ? S.val[b1] : 0.0));
     }
     __syncthreads();
     if (lane < A.groups) {
       int before = 0;
       for (int g = 0; g < A.groups; ++g)
-        before += group_key[g] > group_key[lane] || (group_key[g] == group_key[lane] && g < lane);
+        before += S.group_key[g] > S.group_key[lane] || (S.group_key[g] == S.group_key[lane] && g < lane);
       if (before >= A.keep)
-        for (int e = lane * per; e < (lane + 1) * per; ++e) key[e] = 0;
+        for (int e = lane * per; e < (lane + 1) * per; ++e) S.key[e] = 0;
     }
     __syncthreads();
   }
@@ -127,7 +168,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, bool normalize) 
     uint64_t k0 = 0;
     int e0 = 1 << 30;
     for (int e = lane; e < A.E; e += 64)
-      if (key[e] > k0) k0 = key[e], e0 = e;
+      if (S.key[e] > k0) k0 = S.key[e], e0 = e;
     for (int d = 32; d; d /= 2) {
       const uint64_t k1 = __shfl_xor(k0, d);
       const int e1 = __shfl_xor(e0, d);
@@ -135,15 +176,16 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, bool normalize) 
     }
     if (k0 == 0) break;
     if (lane == j) mine = e0;
-    if (lane == 0) key[e0] = 0;
+    if (lane == 0) S.key[e0] = 0;
     __syncthreads();
   }
-  const float l = mine < 0 ? -__builtin_inff() : logit<DT>(A.logits, at + mine);
+  __syncthreads();
+  const float l = mine < 0 ? -kInf : logit<DT>(A.logits, at + mine);
   double w;
   if (normalize) {
-    const float first = __any(mine >= 0 && l != l) ? __builtin_nanf("") : wave_max(l);
+    const float first = __any(mine >= 0 && l != l) ? __builtin_nanf("") : token_max<64>(l);
     const double u = mine < 0 ? 0 : share_of_choice<SIGMOID, double>(l, first);
-    w = u / wave_sum(u);
+    w = u / token_sum<64>(u);
     if (!SIGMOID && bad) w = __builtin_nan("");
   } else {
     w = score(l);
@@ -151,6 +193,196 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, bool normalize) 
   if (lane < A.k) {
     A.ids[static_cast<int64_t>(t) * A.k + lane] = mine;
     A.weights[static_cast<int64_t>(t) * A.k + lane] = mine < 0 ? 0.f : static_cast<float>(w * A.scale);
+  }
+}
+
+// L lanes to a token, each with V experts next to each other, so that the lowest of equal experts is
+// in the lowest lane: k rounds of a maximum over a lane's experts and over the lanes (rotations within
+// 16 lanes), in which the winner leaves.  For 256 experts a round costs 84 instructions for the four
+// tokens of a wavefront, against 30 for one token with 64 lanes and 4 experts each.
+//
+// What chooses: where nothing is added to a score, the logits, which order like it.  Otherwise c in
+// float32, with the least distance at which two of its values are sure to be in order; a token with
+// closer ones (among its first k + 1, or about groups) is done again in 64 bits, as is one with NaN.
+// Logits of 16384 tokens over 256 experts in 8 groups: see the table of times.
+//
+// Distances: a sigmoid's float32 value is off by at most 2^-22 (its exponential by (|l| + 1) 2^-23 of
+// itself, which the slope s (1 - s) takes to at most 0.48 * 2^-23; sum, reciprocal and the addition of
+// the bias 2.5 * 2^-24), a softmax's by 2^-20 of the row's largest, most of it from the sum, and c by
+// 2^-24 of itself.  Twice that between two values, twice again for the sums of two; all of it doubled.
+template <int L, int V, bool SIGMOID, bool GROUPS>
+__global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool normalize, bool vectors) {
+  constexpr int N = L * V;
+  __shared__ union {
+    ExactSpace<N> exact;
+    struct {
+      float c[64 / L][N + kMaxExpertGroups];  // a place more after each group: no bank conflicts
+      float score[64 / L][kMaxExpertGroups];
+    } g;
+  } S;
+  const int lane = threadIdx.x, l0 = lane % L, slot = lane / L;
+  const int t0 = blockIdx.x * (64 / L), t = min(t0 + slot, A.n - 1);
+  const int64_t at = t * A.ld + l0 * V;
+  const int mine_n = min(V, A.E - l0 * V);  // may be negative
+  float l[V];
+  auto fetch = [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+    constexpr int W = DT == SGMV_F32 ? 4 : 8;  // elements of 16 bytes
+    if (V % W == 0 && vectors && mine_n == V) {
+#pragma unroll
+      for (int v = 0; v + W <= V; v += W) {
+        if constexpr (DT == SGMV_F32) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(A.logits) + at + v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[v + i] = x[i];
+        } else {
+          const uint4 x = ld16(static_cast<const uint16_t*>(A.logits) + at + v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[v + i] = elem<DT>(x, i);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = v < mine_n ? logit<DT>(A.logits, at + v) : -kInf;
+    }
+  };
+  if (dtype == SGMV_F32) fetch(std::integral_constant<int, SGMV_F32>{});
+  else if (dtype == SGMV_F16) fetch(std::integral_constant<int, SGMV_F16>{});
+  else fetch(std::integral_constant<int, SGMV_BF16>{});
+
+  const bool by_logit = !A.bias && (!GROUPS || A.best == 1);
+  bool open = false;  // to be done in 64 bits
+  float top = -kInf, sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    open |= SIGMOID ? l[v] != l[v] : !(l[v] < kInf);
+    top = fmaxf(top, l[v]);
+  }
+  float c[V], near = 0.f;
+  if (!SIGMOID && (!by_logit || !normalize)) {
+    top = token_max<L>(top);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      c[v] = l[v] == -kInf ? 0.f : __expf(l[v] - top);
+      sum += c[v];
+    }
+    sum = token_sum<L>(sum);
+  }
+  if (by_logit) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = l[v];
+  } else {
+    const float one = 1.f / sum;  // the largest score
+    near = SIGMOID ? 0x1p-20f : 0x1p-18f * one;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float s = SIGMOID ? __builtin_amdgcn_rcpf(1.f + __expf(-l[v])) : c[v] * one;
+      const float b = A.bias && v < mine_n ? A.bias[l0 * V + v] : 0.f;
+      c[v] = l[v] == -kInf ? -kInf : s + b;
+      open |= c[v] != c[v];
+    }
+  }
+  const auto apart = [&](float a) { return by_logit ? 0.f : near + 0x1p-21f * fabsf(a); };
+
+  if constexpr (GROUPS) {
+    const int per = A.E / A.groups;
+    float* const row = S.g.c[slot];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = l0 * V + v;
+      if (v < mine_n) row[e + e / per] = c[v];
+    }
+    __syncthreads();
+    for (int g = l0; g < A.groups; g += L) {
+      float b0 = -kInf, b1 = -kInf;
+      for (int e = 0; e < per; ++e) {
+        const float x = row[g * (per + 1) + e];
+        b1 = fmaxf(b1, fminf(b0, x));
+        b0 = fmaxf(b0, x);
+      }
+      S.g.score[slot][g] = A.best > 1 && b1 > -kInf ? b0 + b1 : b0;
+    }
+    __syncthreads();
+    uint64_t kept = 0;
+    for (int g0 = 0; g0 < A.groups; g0 += L) {
+      const int g = g0 + l0;
+      bool stay = false;
+      if (g < A.groups) {
+        const float mine = S.g.score[slot][g], d = 2 * apart(mine);
+        int before = 0, after = 0;  // surely better ones, and those that may be
+        for (int h = 0; h < A.groups; ++h) {
+          const float other = S.g.score[slot][h];
+          before += other > mine || (other == mine && h < g);
+          if (h != g && fabsf(other - mine) <= d && mine > -kInf && !by_logit) ++after;
+        }
+        stay = before < A.keep;
+        // a close one on the other side of the cut
+        if (after && before + after >= A.keep && before - after < A.keep) open = true;
+      }
+      const uint64_t set = __ballot(stay);
+      kept |= (L == 64 ? set : set >> (lane & 48) & 0xffffu) << g0;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < mine_n && !(kept >> ((l0 * V + v) / per) & 1)) c[v] = -kInf;
+    __syncthreads();
+  }
+
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) key[v] = order(c[v]);
+  int mine = -1;  // lane j of a token: its j-th expert
+  uint32_t last = 0;
+  for (int j = 0; j < A.k + !by_logit; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    const uint32_t m = over_token<L>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+    if (!by_logit && j > 0 && m) {
+      // back to the values that the keys stand for
+      const auto value = [](uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); };
+      open |= !(value(last) - value(m) > apart(value(last)));
+    }
+    last = m;
+    if (j == A.k) break;
+    const uint64_t set = __ballot(best == m);
+    const int first = __builtin_ctzll(L == 64 ? set : set >> (lane & 48) & 0xffffu);
+    int v0 = 0;
+#pragma unroll
+    for (int v = V - 1; v > 0; --v) v0 = key[v] == m ? v : v0;
+    v0 = key[0] == m ? 0 : v0;
+    const int e = from_lane(l0 * V + v0, (lane - l0) + first);
+    if (l0 == j) mine = m ? e : -1;
+    const int leaves = l0 == first ? v0 : V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = v == leaves ? 0u : key[v];
+  }
+
+  const int64_t to = static_cast<int64_t>(t) * A.k + l0;
+  const int64_t own = t * A.ld + mine;
+  const float x = mine < 0 ? -kInf : dtype == SGMV_F32   ? logit<SGMV_F32>(A.logits, own)
+                                     : dtype == SGMV_F16 ? logit<SGMV_F16>(A.logits, own)
+                                                         : logit<SGMV_BF16>(A.logits, own);
+  float w;
+  if (normalize) {
+    const float first = token_max<L>(x);  // by all lanes
+    const float u = mine < 0 ? 0.f : share_of_choice<SIGMOID, float>(x, first);
+    w = u / token_sum<L>(u);
+  } else {
+    w = SIGMOID ? share_of_choice<SIGMOID, float>(x, 0.f) : expf(x - top) / sum;
+  }
+  open = token_any<L>(open);
+  if (l0 < A.k && t0 + slot < A.n && !open) {
+    A.ids[to] = mine;
+    A.weights[to] = mine < 0 ? 0.f : w * A.scale;
+  }
+  const uint64_t again = __ballot(open && l0 == 0 && t0 + slot < A.n);
+  for (int s = 0; s < 64 / L; ++s) {
+    if (!(again >> (s * L) & 1)) continue;
+    __syncthreads();
+    if (dtype == SGMV_F32) route_exactly<SGMV_F32, SIGMOID>(A, t0 + s, normalize, S.exact);
+    else if (dtype == SGMV_F16) route_exactly<SGMV_F16, SIGMOID>(A, t0 + s, normalize, S.exact);
+    else route_exactly<SGMV_BF16, SIGMOID>(A, t0 + s, normalize, S.exact);
   }
 }
 
@@ -165,57 +397,76 @@ struct RouteBackArgs {
   float scale;
 };
 
-template <int DT, bool SIGMOID>
-__global__ __launch_bounds__(64) void route_backward_kernel(RouteBackArgs A, bool normalize) {
-  __shared__ float d[kMaxGroups];
-  const int lane = threadIdx.x, t = blockIdx.x;
+// L lanes to a token; lane j has its j-th choice.  The row is put together in LDS and written in whole
+// pieces; only a softmax that is not normalised reads all of it.
+template <int DT, bool SIGMOID, int L, int N>
+__global__ __launch_bounds__(64) void route_backward_kernel(RouteBackArgs A, bool normalize, bool vectors) {
+  __shared__ __attribute__((aligned(16))) float rows[64 / L][N];
+  const int lane = threadIdx.x, l0 = lane % L, slot = lane / L;
+  const int t = min(static_cast<int>(blockIdx.x) * (64 / L) + slot, A.n - 1);
   const int64_t at = t * A.ld, to = t * A.ld_d;
-  const int id = lane < A.k ? A.ids[static_cast<int64_t>(t) * A.k + lane] : -1;
-  const float l = static_cast<uint32_t>(id) < static_cast<uint32_t>(A.E) ? logit<DT>(A.logits, at + id)
-                                                                         : -__builtin_inff();
-  const bool in = l != -__builtin_inff();  // takes part
-  const float g = in ? A.scale * A.dweights[static_cast<int64_t>(t) * A.k + lane] : 0.f;
-  float top = -__builtin_inff(), sum = 0.f, mine = 0.f, inner = 0.f;
-  if (!SIGMOID && !normalize) {
+  float* const row = rows[slot];
+  const int id = l0 < A.k ? A.ids[static_cast<int64_t>(t) * A.k + l0] : -1;
+  const float l = static_cast<uint32_t>(id) < static_cast<uint32_t>(A.E) ? logit<DT>(A.logits, at + id) : -kInf;
+  const bool in = l != -kInf;  // takes part
+  const float g = in ? A.scale * A.dweights[static_cast<int64_t>(t) * A.k + l0] : 0.f;
+  const bool whole = !SIGMOID && !normalize;
+  float top = -kInf, sum = 0.f, mine = 0.f, inner = 0.f;
+  if (whole) {
     bool bad = false;
-    for (int e = lane; e < A.E; e += 64) {
+    for (int e = l0; e < A.E; e += L) {
       const float v = logit<DT>(A.logits, at + e);
-      bad |= !(v < __builtin_inff());
+      bad |= !(v < kInf);
       top = fmaxf(top, v);
     }
-    top = wave_max(top);
-    for (int e = lane; e < A.E; e += 64) {
+    top = token_max<L>(top);
+    for (int e = l0; e < A.E; e += L) {
       const float v = logit<DT>(A.logits, at + e);
-      if (v != -__builtin_inff()) sum += expf(v - top);
+      if (v != -kInf) sum += expf(v - top);
     }
-    sum = wave_sum(sum);
-    if (__any(bad)) sum = __builtin_nanf("");
-    inner = wave_sum(in ? g * (expf(l - top) / sum) : 0.f);
+    sum = token_sum<L>(sum);
+    if (token_any<L>(bad)) sum = __builtin_nanf("");
+    inner = token_sum<L>(in ? g * (expf(l - top) / sum) : 0.f);
     mine = g;
   } else if (normalize) {
-    top = __any(in && l != l) ? __builtin_nanf("") : wave_max(l);
+    const bool bad = token_any<L>(in && l != l);
+    top = token_max<L>(l);
+    if (bad) top = __builtin_nanf("");
     float u = in ? share_of_choice<SIGMOID, float>(l, top) : 0.f;
-    u /= wave_sum(u);
-    inner = wave_sum(in ? g * u : 0.f);
+    u /= token_sum<L>(u);
+    inner = token_sum<L>(in ? g * u : 0.f);
     mine = in ? u * (g - inner) * (SIGMOID ? 1.f / (1.f + expf(l)) : 1.f) : 0.f;
   } else {
-    mine = in ? g * (1.f / (1.f + expf(-l))) * (1.f / (1.f + expf(l))) : 0.f;
+    mine = in ? g * share_of_choice<SIGMOID, float>(l, 0.f) * (1.f / (1.f + expf(l))) : 0.f;
   }
-  for (int e = lane; e < A.E; e += 64) d[e] = 0.f;
+  for (int e = 4 * l0; e < N; e += 4 * L) *reinterpret_cast<f32x4_t*>(&row[e]) = f32x4_t{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
   // one at a time, in order: the same expert may stand twice
   for (int j = 0; j < A.k; ++j) {
-    if (lane == j && in) d[id] += mine;
+    if (l0 == j && in) row[id] += mine;
     __syncthreads();
   }
-  for (int e = lane; e < A.E; e += 64) {
-    float v = d[e];
-    if (!SIGMOID && !normalize) {
-      const float x = logit<DT>(A.logits, at + e);
-      v = x == -__builtin_inff() ? 0.f : expf(x - top) / sum * (v - inner);
+  if (static_cast<int>(blockIdx.x) * (64 / L) + slot >= A.n) return;
+  const auto value = [&](int e) {
+    const float v = row[e];
+    if (!whole) return v;
+    const float x = logit<DT>(A.logits, at + e);
+    return x == -kInf ? 0.f : expf(x - top) / sum * (v - inner);
+  };
+  constexpr int W = DT == SGMV_F32 ? 4 : 8;  // elements of 16 bytes
+  const int tail = vectors ? A.E / W * W : 0;
+  for (int e = W * l0; e < tail; e += W * L) {
+    if constexpr (DT == SGMV_F32) {
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.dlogits) + to + e) =
+          f32x4_t{value(e), value(e + 1), value(e + 2), value(e + 3)};
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = Elem<DT>::pack(value(e + 2 * i), value(e + 2 * i + 1));
+      store_words<4>(static_cast<uint16_t*>(A.dlogits) + to + e, o);
     }
-    store_logit<DT>(A.dlogits, to + e, v);
   }
+  for (int e = tail + l0; e < A.E; e += L) store_logit<DT>(A.dlogits, to + e, value(e));
 }
 
 // ------------------------------------------------------------------------------------
@@ -274,10 +525,49 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs A) {
     for (int i = 0; i < 4; ++i) o[i] = Elem<DT>::pack(w * elem<DT>(d, 2 * i), w * elem<DT>(d, 2 * i + 1));
     store_words<4>(A.out + row * A.ld_out + c, o);
   }
-  dot = wave_sum(dot);
+  dot = token_sum<64>(dot);
   if (lane == 0) sums[threadIdx.x / 64] = dot;
   __syncthreads();
   if (A.dweights && threadIdx.x == 0) A.dweights[row] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// ------------------------------------------------------------------------------------
+// launches
+// ------------------------------------------------------------------------------------
+// 16 lanes to a token, up to 256 experts of which up to 16 are chosen; 64 otherwise.
+template <int L, int V, bool SIGMOID>
+void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, bool vectors) {
+  const int grid = static_cast<int>(tiles_of(A.n, 64 / L));
+  if (A.keep < A.groups) route_kernel<L, V, SIGMOID, true><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors);
+  else route_kernel<L, V, SIGMOID, false><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors);
+}
+template <bool SIGMOID>
+void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, bool vectors) {
+  const auto go = [&](auto lanes, auto each) {
+    launch_route<decltype(lanes)::value, decltype(each)::value, SIGMOID>(s, A, dtype, normalize, vectors);
+  };
+  using std::integral_constant;
+  const integral_constant<int, 16> some{};
+  const integral_constant<int, 64> all{};
+  if (A.k > 16 || A.E > 256) {
+    if (A.E <= 256) go(all, integral_constant<int, 4>{});
+    else go(all, integral_constant<int, 16>{});
+  } else if (A.E <= 32) go(some, integral_constant<int, 2>{});
+  else if (A.E <= 64) go(some, integral_constant<int, 4>{});
+  else if (A.E <= 128) go(some, integral_constant<int, 8>{});
+  else go(some, integral_constant<int, 16>{});
+}
+
+template <int DT>
+void launch_back(hipStream_t s, const RouteBackArgs& A, int32_t scores, bool normalize, bool vectors) {
+  const auto go = [&](auto kernel, int lanes) {
+    kernel<<<static_cast<int>(tiles_of(A.n, 64 / lanes)), 64, 0, s>>>(A, normalize, vectors);
+  };
+  const bool sigmoid = scores == SGMV_SIGMOID;
+  if (A.k > 16 || A.E > 256)
+    go(sigmoid ? route_backward_kernel<DT, true, 64, kMaxGroups> : route_backward_kernel<DT, false, 64, kMaxGroups>, 64);
+  else
+    go(sigmoid ? route_backward_kernel<DT, true, 16, 256> : route_backward_kernel<DT, false, 16, 256>, 16);
 }
 
 // ------------------------------------------------------------------------------------
@@ -330,11 +620,9 @@ extern "C" int sgmv_route(hipStream_t stream, int32_t dtype, int32_t* ids, float
       return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
   const RouteArgs A{logits, ld_logits, bias, ids, weights, n, n_experts, k, expert_groups, keep_groups, group_best, scale};
-  const auto go = [&](auto kernel) { kernel<<<n, 64, 0, stream>>>(A, normalize != 0); };
-  const bool sigmoid = scores == SGMV_SIGMOID;
-  if (dtype == SGMV_F32) go(sigmoid ? route_kernel<SGMV_F32, true> : route_kernel<SGMV_F32, false>);
-  else if (dtype == SGMV_F16) go(sigmoid ? route_kernel<SGMV_F16, true> : route_kernel<SGMV_F16, false>);
-  else go(sigmoid ? route_kernel<SGMV_BF16, true> : route_kernel<SGMV_BF16, false>);
+  const bool vectors = aligned16(logits) && ld_logits * elem_bytes(dtype) % 16 == 0;
+  if (scores == SGMV_SIGMOID) launch_route<true>(stream, A, dtype, normalize != 0, vectors);
+  else launch_route<false>(stream, A, dtype, normalize != 0, vectors);
   return hip_status(hipGetLastError());
 }
 
@@ -355,11 +643,10 @@ extern "C" int sgmv_route_backward(hipStream_t stream, int32_t dtype, void* dlog
     return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
   const RouteBackArgs A{logits, ld_logits, ids, dweights, dlogits, ld_dlogits, n, n_experts, k, scale};
-  const auto go = [&](auto kernel) { kernel<<<n, 64, 0, stream>>>(A, normalize != 0); };
-  const bool sigmoid = scores == SGMV_SIGMOID;
-  if (dtype == SGMV_F32) go(sigmoid ? route_backward_kernel<SGMV_F32, true> : route_backward_kernel<SGMV_F32, false>);
-  else if (dtype == SGMV_F16) go(sigmoid ? route_backward_kernel<SGMV_F16, true> : route_backward_kernel<SGMV_F16, false>);
-  else go(sigmoid ? route_backward_kernel<SGMV_BF16, true> : route_backward_kernel<SGMV_BF16, false>);
+  const bool vectors = aligned16(dlogits) && ld_dlogits * one % 16 == 0;
+  if (dtype == SGMV_F32) launch_back<SGMV_F32>(stream, A, scores, normalize != 0, vectors);
+  else if (dtype == SGMV_F16) launch_back<SGMV_F16>(stream, A, scores, normalize != 0, vectors);
+  else launch_back<SGMV_BF16>(stream, A, scores, normalize != 0, vectors);
   return hip_status(hipGetLastError());
 }
 
