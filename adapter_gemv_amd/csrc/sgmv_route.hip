@@ -31,39 +31,42 @@ __device__ inline float logit(const void* p, int64_t i) {
   if constexpr (DT == SGMV_F32) return static_cast<const float*>(p)[i];
   else return Elem<DT>::lo(static_cast<const uint16_t*>(p)[i]);
 }
+__device__ inline float logit(int dtype, const void* p, int64_t i) {
+  return dtype == SGMV_F32 ? logit<SGMV_F32>(p, i) : dtype == SGMV_F16 ? logit<SGMV_F16>(p, i) : logit<SGMV_BF16>(p, i);
+}
 template <int DT>
 __device__ inline void store_logit(void* p, int64_t i, float v) {
   if constexpr (DT == SGMV_F32) static_cast<float*>(p)[i] = v;
   else static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(Elem<DT>::pack(v, 0.f));
 }
 
-// Reductions over the L lanes of a token (16: a row of the wavefront, by rotations within it), in every
-// lane; all of them have to take part.
-template <typename T>
-__device__ inline T from_lane(T v, int lane) { return __shfl(v, lane); }
+// Reductions over the L lanes of a token (16: a row of the wavefront, by rotations within it; 64: then
+// across rows), in every lane; all of them have to take part.
+__device__ inline int from_lane(int v, int lane) { return __shfl(v, lane); }
 template <int CTRL>
 __device__ inline uint32_t rotated(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 15, 15, false));
 }
 template <int L, typename T, typename F>
 __device__ inline T over_token(T v, F op) {
-  static_assert(L == 16 || L == 64, "");
+  static_assert((L == 16 || L == 64) && (sizeof(T) == 4 || sizeof(T) == 8), "");
   if constexpr (sizeof(T) == 4) {
     constexpr int kRotate = 0x120;  // row_ror
-    const auto turn = [](T x, auto by) {
-      return __builtin_bit_cast(T, rotated<kRotate + decltype(by)::value>(__builtin_bit_cast(uint32_t, x)));
-    };
-    v = op(v, turn(v, std::integral_constant<int, 8>{}));
-    v = op(v, turn(v, std::integral_constant<int, 4>{}));
-    v = op(v, turn(v, std::integral_constant<int, 2>{}));
-    v = op(v, turn(v, std::integral_constant<int, 1>{}));
+    const auto bits = [](T x) { return __builtin_bit_cast(uint32_t, x); };
+    const auto back = [](uint32_t x) { return __builtin_bit_cast(T, x); };
+    v = op(v, back(rotated<kRotate + 8>(bits(v))));
+    v = op(v, back(rotated<kRotate + 4>(bits(v))));
+    v = op(v, back(rotated<kRotate + 2>(bits(v))));
+    v = op(v, back(rotated<kRotate + 1>(bits(v))));
+    if constexpr (L == 64) {
+      const auto h = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+      v = op(back(h[0]), back(h[1]));
+      const auto q = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+      v = op(back(q[0]), back(q[1]));
+    }
   } else {
 #pragma unroll
-    for (int d = 8; d; d /= 2) v = op(v, __shfl_xor(v, d));
-  }
-  if constexpr (L == 64) {
-    v = op(v, __shfl_xor(v, 16));
-    v = op(v, __shfl_xor(v, 32));
+    for (int d = 1; d < L; d *= 2) v = op(v, __shfl_xor(v, d));
   }
   return v;
 }
@@ -74,6 +77,10 @@ __device__ inline T token_sum(T v) {
 template <int L>
 __device__ inline float token_max(float v) {
   return over_token<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ inline uint32_t token_most(uint32_t v) {
+  return over_token<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int L>
 __device__ inline bool token_any(bool v) {
@@ -111,14 +118,14 @@ struct ExactSpace {
   double val[N];
   uint64_t group_key[kMaxExpertGroups];
 };
-template <int DT, bool SIGMOID, int N>
-__device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, ExactSpace<N>& S) {
+template <bool SIGMOID, int N>
+__device__ __forceinline__ void route_exactly(const RouteArgs& A, int dtype, int t, bool normalize, ExactSpace<N>& S) {
   const int lane = threadIdx.x;
   const int64_t at = t * A.ld;
   float top = -kInf;
   bool bad = false;
   for (int e = lane; e < A.E; e += 64) {
-    const float l = logit<DT>(A.logits, at + e);
+    const float l = logit(dtype, A.logits, at + e);
     bad |= !(l < kInf);
     top = fmaxf(top, l);
   }
@@ -126,7 +133,7 @@ __device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, E
   top = token_max<64>(top);
   double sum = 0;
   if (!SIGMOID) {
-    for (int e = lane; e < A.E; e += 64) sum += exp(static_cast<double>(logit<DT>(A.logits, at + e)) - top);
+    for (int e = lane; e < A.E; e += 64) sum += exp(static_cast<double>(logit(dtype, A.logits, at + e)) - top);
     sum = token_sum<64>(sum);
   }
   auto score = [&](float l) -> double {
@@ -135,7 +142,7 @@ __device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, E
   };
   const bool by_logit = !A.bias && (A.keep == A.groups || A.best == 1);
   for (int e = lane; e < A.E; e += 64) {
-    const float l = logit<DT>(A.logits, at + e);
+    const float l = logit(dtype, A.logits, at + e);
     const double c = by_logit ? (!SIGMOID && bad ? __builtin_nan("") : static_cast<double>(l))
                               : score(l) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0);
     S.key[e] = l == -kInf || c == -__builtin_inf() ? 0 : order(c);
@@ -145,13 +152,19 @@ __device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, E
   if (A.keep < A.groups) {
     const int per = A.E / A.groups;
     if (lane < A.groups) {
-      int b0 = -1, b1 = -1;
+      // the two best, as keys and where they are (no two places of one key: the first)
+      uint64_t k0 = 0, k1 = 0;
+      int b0 = 0, b1 = 0;
+#pragma unroll 4
       for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        if (S.key[e] == 0) continue;
-        if (b0 < 0 || S.key[e] > S.key[b0]) b1 = b0, b0 = e;
-        else if (b1 < 0 || S.key[e] > S.key[b1]) b1 = e;
+        const uint64_t k = S.key[e];
+        const bool first = k > k0, second = k > k1;
+        k1 = first ? k0 : second ? k : k1;
+        b1 = first ? b0 : second ? e : b1;
+        k0 = first ? k : k0;
+        b0 = first ? e : b0;
       }
-      S.group_key[lane] = b0 < 0 ? 0 : order(S.val[b0] + (A.best > 1 && b1 >= 0 ? S.val[b1] : 0.0));
+      S.group_key[lane] = k0 == 0 ? 0 : order(S.val[b0] + (A.best > 1 && k1 != 0 ? S.val[b1] : 0.0));
     }
     __syncthreads();
     if (lane < A.groups) {
@@ -169,18 +182,18 @@ __device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, E
     int e0 = 1 << 30;
     for (int e = lane; e < A.E; e += 64)
       if (S.key[e] > k0) k0 = S.key[e], e0 = e;
-    for (int d = 32; d; d /= 2) {
-      const uint64_t k1 = __shfl_xor(k0, d);
-      const int e1 = __shfl_xor(e0, d);
-      if (k1 > k0 || (k1 == k0 && e1 < e0)) k0 = k1, e0 = e1;
-    }
-    if (k0 == 0) break;
+    // the largest key, by halves, and the lowest place that has it
+    const uint32_t high = token_most<64>(static_cast<uint32_t>(k0 >> 32));
+    const uint32_t low = token_most<64>(static_cast<uint32_t>(k0 >> 32) == high ? static_cast<uint32_t>(k0) : 0u);
+    const uint64_t k = static_cast<uint64_t>(high) << 32 | low;
+    e0 = static_cast<int>(~token_most<64>(k0 == k ? ~static_cast<uint32_t>(e0) : 0u));
+    if (k == 0) break;
     if (lane == j) mine = e0;
     if (lane == 0) S.key[e0] = 0;
     __syncthreads();
   }
   __syncthreads();
-  const float l = mine < 0 ? -kInf : logit<DT>(A.logits, at + mine);
+  const float l = mine < 0 ? -kInf : logit(dtype, A.logits, at + mine);
   double w;
   if (normalize) {
     const float first = __any(mine >= 0 && l != l) ? __builtin_nanf("") : token_max<64>(l);
@@ -211,7 +224,8 @@ __device__ __noinline__ void route_exactly(RouteArgs A, int t, bool normalize, E
 // the bias 2.5 * 2^-24), a softmax's by 2^-20 of the row's largest, most of it from the sum, and c by
 // 2^-24 of itself.  Twice that between two values, twice again for the sums of two; all of it doubled.
 template <int L, int V, bool SIGMOID, bool GROUPS>
-__global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool normalize, bool vectors) {
+__global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool normalize, bool vectors,
+                                                   bool bias_vectors) {
   constexpr int N = L * V;
   __shared__ union {
     ExactSpace<N> exact;
@@ -274,11 +288,22 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
   } else {
     const float one = 1.f / sum;  // the largest score
     near = SIGMOID ? 0x1p-20f : 0x1p-18f * one;
+    float b[V];
+    if (V % 4 == 0 && bias_vectors && mine_n == V) {
+#pragma unroll
+      for (int v = 0; v + 4 <= V; v += 4) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(A.bias + l0 * V + v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[v + i] = x[i];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) b[v] = A.bias && v < mine_n ? A.bias[l0 * V + v] : 0.f;
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float s = SIGMOID ? __builtin_amdgcn_rcpf(1.f + __expf(-l[v])) : c[v] * one;
-      const float b = A.bias && v < mine_n ? A.bias[l0 * V + v] : 0.f;
-      c[v] = l[v] == -kInf ? -kInf : s + b;
+      c[v] = l[v] == -kInf ? -kInf : s + b[v];
       open |= c[v] != c[v];
     }
   }
@@ -287,14 +312,16 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
   if constexpr (GROUPS) {
     const int per = A.E / A.groups;
     float* const row = S.g.c[slot];
+    const int g0 = l0 * V / per, in0 = l0 * V - g0 * per;  // this lane's first group, and place in it
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = l0 * V + v;
-      if (v < mine_n) row[e + e / per] = c[v];
+    for (int v = 0, g = g0, in = in0; v < V; ++v) {
+      if (v < mine_n) row[l0 * V + v + g] = c[v];
+      if (++in == per) in = 0, ++g;
     }
     __syncthreads();
     for (int g = l0; g < A.groups; g += L) {
       float b0 = -kInf, b1 = -kInf;
+#pragma unroll 8
       for (int e = 0; e < per; ++e) {
         const float x = row[g * (per + 1) + e];
         b1 = fmaxf(b1, fminf(b0, x));
@@ -304,8 +331,8 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
     }
     __syncthreads();
     uint64_t kept = 0;
-    for (int g0 = 0; g0 < A.groups; g0 += L) {
-      const int g = g0 + l0;
+    for (int first = 0; first < A.groups; first += L) {
+      const int g = first + l0;
       bool stay = false;
       if (g < A.groups) {
         const float mine = S.g.score[slot][g], d = 2 * apart(mine);
@@ -320,11 +347,13 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
         if (after && before + after >= A.keep && before - after < A.keep) open = true;
       }
       const uint64_t set = __ballot(stay);
-      kept |= (L == 64 ? set : set >> (lane & 48) & 0xffffu) << g0;
+      kept |= (L == 64 ? set : set >> (lane & 48) & 0xffffu) << first;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < mine_n && !(kept >> ((l0 * V + v) / per) & 1)) c[v] = -kInf;
+    for (int v = 0, g = g0, in = in0; v < V; ++v) {
+      if (!(kept >> (g & 63) & 1)) c[v] = -kInf;
+      if (++in == per) in = 0, ++g;
+    }
     __syncthreads();
   }
 
@@ -337,7 +366,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
     uint32_t best = key[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) best = max(best, key[v]);
-    const uint32_t m = over_token<L>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+    const uint32_t m = token_most<L>(best);
     if (!by_logit && j > 0 && m) {
       // back to the values that the keys stand for
       const auto value = [](uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); };
@@ -360,9 +389,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
 
   const int64_t to = static_cast<int64_t>(t) * A.k + l0;
   const int64_t own = t * A.ld + mine;
-  const float x = mine < 0 ? -kInf : dtype == SGMV_F32   ? logit<SGMV_F32>(A.logits, own)
-                                     : dtype == SGMV_F16 ? logit<SGMV_F16>(A.logits, own)
-                                                         : logit<SGMV_BF16>(A.logits, own);
+  const float x = mine < 0 ? -kInf : logit(dtype, A.logits, own);
   float w;
   if (normalize) {
     const float first = token_max<L>(x);  // by all lanes
@@ -380,9 +407,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
   for (int s = 0; s < 64 / L; ++s) {
     if (!(again >> (s * L) & 1)) continue;
     __syncthreads();
-    if (dtype == SGMV_F32) route_exactly<SGMV_F32, SIGMOID>(A, t0 + s, normalize, S.exact);
-    else if (dtype == SGMV_F16) route_exactly<SGMV_F16, SIGMOID>(A, t0 + s, normalize, S.exact);
-    else route_exactly<SGMV_BF16, SIGMOID>(A, t0 + s, normalize, S.exact);
+    route_exactly<SIGMOID>(A, dtype, t0 + s, normalize, S.exact);
   }
 }
 
@@ -538,8 +563,9 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs A) {
 template <int L, int V, bool SIGMOID>
 void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, bool vectors) {
   const int grid = static_cast<int>(tiles_of(A.n, 64 / L));
-  if (A.keep < A.groups) route_kernel<L, V, SIGMOID, true><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors);
-  else route_kernel<L, V, SIGMOID, false><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors);
+  const bool bias_vectors = A.bias && aligned16(A.bias);
+  if (A.keep < A.groups) route_kernel<L, V, SIGMOID, true><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors, bias_vectors);
+  else route_kernel<L, V, SIGMOID, false><<<grid, 64, 0, s>>>(A, dtype, normalize, vectors, bias_vectors);
 }
 template <bool SIGMOID>
 void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, bool vectors) {
