@@ -16,7 +16,7 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check, check_sizes
-from .grouped import RowGroups, _ld, _on, _share, _stream_of, _tables
+from .grouped import RowGroups, _empty, _ld, _share, _stream_of, _tables
 from .mx import _as_rows
 from .sgmv import _check_rows, _torch, dtype_code
 
@@ -25,14 +25,6 @@ BLOCK = 128
 
 def _blocks(h: int) -> int:
     return (h + BLOCK - 1) // BLOCK
-
-
-def _empty(like, shape, dtype, stream):
-    """An allocation on ``like``'s device for work on ``stream``."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with _on(stream):
-        return like.new_empty(shape, dtype=dtype)
 
 
 def _made(kind, codes, scales):
@@ -194,7 +186,7 @@ def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: b
             lib.sgmv_block_workspace_bytes(n, share, E, starts is not None, h_in, h_out))
     at = None
     if room:
-        space = _empty(out, room, _torch().uint8, stream)
+        space = _empty(out, (room,), _torch().uint8, stream)
         at = space.data_ptr()
     head = (handle, dt, out.data_ptr(), _ld(out), rows.data_ptr(), _ld(rows))
     st = (lib.sgmv_block_matmul_dx(*head, *tail, at, room) if dx else

@@ -33,6 +33,14 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
+def _empty(like, shape, dtype, stream):
+    """A dense allocation on ``like``'s device, for work on ``stream``."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _stream_of(stream, *tensors) -> int:
     """The handle of ``stream`` (None: the current one), once every tensor is known to be on the
     current GPU, where the kernels are launched.  (The raw handle is taken directly: building a
@@ -42,7 +50,7 @@ def _stream_of(stream, *tensors) -> int:
     for t in tensors:
         if t.get_device() != here:
             raise ValueError("tensors must be on one GPU")
-    if here < 0 or here != torch.cuda.current_device():
+    if here < 0 or here != torch._C._cuda_getDevice():
         raise ValueError("tensors must be on the current GPU")
     return torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream.cuda_stream)
 

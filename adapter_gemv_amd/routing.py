@@ -21,7 +21,7 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check, check_sizes
-from .grouped import _ld, _on, _stream_of
+from .grouped import _empty, _ld, _stream_of
 from .sgmv import _check_rows, _torch, dtype_code
 
 SCORES = {"softmax": _lib.SOFTMAX, "sigmoid": _lib.SIGMOID}
@@ -39,9 +39,9 @@ class Routes:
 
 
 def _logits_code(t, name: str) -> int:
-    if t.dim() != 2 or t.shape[1] == 0 or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2 or not t.is_contiguous() and t.stride(1) != 1 and t.shape[1] > 1 or t.shape[1] == 0:
         raise ValueError(f"{name} must be [T, E] with unit column stride")
-    return _lib.F32 if t.dtype == _torch().float32 else dtype_code(t)
+    return _lib.F32 if t.dtype is _torch().float32 else dtype_code(t)
 
 
 def _scores_code(scores: str) -> int:
@@ -51,7 +51,7 @@ def _scores_code(scores: str) -> int:
 
 
 def _dense(t, dtype, shape, name: str):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a dense {str(dtype).split('.')[-1]} tensor {list(shape)}")
 
 
@@ -77,9 +77,8 @@ def route(logits, k: int, *, bias=None, scores: str = "softmax", expert_groups: 
         handle = _stream_of(stream, logits, bias)
     else:
         handle = _stream_of(stream, logits)
-    with _on(stream):
-        ids = logits.new_empty((T, k), dtype=torch.int32)
-        weights = logits.new_empty((T, k), dtype=torch.float32)
+    ids = _empty(logits, (T, k), torch.int32, stream)
+    weights = _empty(logits, (T, k), torch.float32, stream)
     st = _lib.lib().sgmv_route(handle, dt, ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
                                _ld(logits), None if bias is None else bias.data_ptr(), T, E, k,
                                expert_groups, keep, group_best, code, bool(normalize), scale)
@@ -114,23 +113,24 @@ def route_backward(dlogits, dweights, logits, routes: Routes, stream=None):
 
 def _tokens(out, y, weights, what: str):
     """(T, k, h, dtype) of a call whose rows are y [T * k, h] and whose tokens are out [T, h]."""
-    T, n = int(out.shape[0]), int(y.shape[0])
+    if out.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"{what} and the experts' rows must be matrices")
+    (T, h), (n, width) = out.shape, y.shape
     _check_rows(out, T, what)
     _check_rows(y, n, "the experts' rows")
-    if out.shape[1] != y.shape[1]:
-        raise ValueError(f"{what} [., {out.shape[1]}] and the experts' rows [., {y.shape[1]}] do not match")
-    if out.dtype != y.dtype:
+    if width != h:
+        raise ValueError(f"{what} [., {h}] and the experts' rows [., {width}] do not match")
+    if out.dtype is not y.dtype:
         raise TypeError("all rows must share a dtype")
+    k = n // T if T else 1
     if weights is not None:
         if weights.dim() != 2:
             raise ValueError(f"weights must be [{T}, k]")
-        k = int(weights.shape[1])
+        if not T:
+            k = weights.shape[1]
         _dense(weights, _torch().float32, (T, k), "weights")
-    else:
-        k = n // T if T else 1
     if n != T * k or k < 1:
         raise ValueError(f"{n} rows are not the experts' of {T} tokens")
-    h = int(y.shape[1])
     check_sizes("sgmv_combine_rows", n, k, h)
     return T, k, h, dtype_code(y)
 
