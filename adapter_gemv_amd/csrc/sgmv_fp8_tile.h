@@ -285,29 +285,42 @@ __global__ __launch_bounds__(64 * WR * WC, BUFS * BR >= 512 && BR < 256 ? 1 : 2)
       issue_s(sbuf(k), decltype(k)::value);
     });
     wait_tile<(BUFS - 2) * (LOADS + 1)>();
-    rv[0] = rfrag(rbuf(std::integral_constant<int, 0>{}), 0);
-#pragma unroll
-    for (int j = 0; j < NC; ++j) cv[j] = cfrag(cbuf(std::integral_constant<int, 0>{}), j);
-    read_scales(sbuf(std::integral_constant<int, 0>{}));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = CARRY; i < NR; ++i) carried[i] = 0.f;
-    // stage s + k, k of a round.  The buffer that it fills is the one that the stage before read.
+    // stages in rounds.  No branch inside the loop, which keeps the accumulators where they are.
     constexpr int ROUND = BUFS > 4 ? BUFS : 4;
-    auto nth = [&](auto which, int s) __attribute__((always_inline)) {
-      constexpr int k = decltype(which)::value;
-      using Next = std::integral_constant<int, k + 1>;
-      using Fill = std::integral_constant<int, k + BUFS - 1>;
-      stage(rbuf(which), rbuf(Next{}), cbuf(Next{}), sbuf(Next{}), rbuf(Fill{}), cbuf(Fill{}), sbuf(Fill{}), s + k);
+    auto rounds = [&](auto&& nth) __attribute__((always_inline)) {
+      int s = 0;
+      for (; s + ROUND <= nst; s += ROUND) tile_for<0, ROUND>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
+      tile_for<0, ROUND - 1>([&](auto k) __attribute__((always_inline)) {
+        if (s + decltype(k)::value < nst) nth(k, s);
+      });
     };
-    // no branch inside the loop, which keeps the accumulators where they are
-    int s = 0;
-    for (; s + ROUND <= nst; s += ROUND) tile_for<0, ROUND>([&](auto k) __attribute__((always_inline)) { nth(k, s); });
-    tile_for<0, ROUND - 1>([&](auto k) __attribute__((always_inline)) {
-      if (s + decltype(k)::value < nst) nth(k, s);
-    });
-    tile_for<LAST - 3, LAST>([&](auto n) __attribute__((always_inline)) { add(n, carried); });
+    // stage s + k, k of a round.  The buffer that it fills is the one that the stage before read.
+    if (wr * NR * 16 >= t.rows) {  // none of the tile's rows: this wavefront only fetches
+      rounds([&](auto which, int s) __attribute__((always_inline)) {
+        constexpr int k = decltype(which)::value;
+        using Fill = std::integral_constant<int, k + BUFS - 1>;
+        tile_for<0, LOADS>([&](auto l) __attribute__((always_inline)) { issue_one(rbuf(Fill{}), cbuf(Fill{}), s + k + BUFS - 1, l); });
+        issue_s(sbuf(Fill{}), s + k + BUFS - 1);
+        wait_tile<(BUFS - 2) * (LOADS + 1)>();
+      });
+    } else {
+      using First = std::integral_constant<int, 0>;
+      rv[0] = rfrag(rbuf(First{}), 0);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) cv[j] = cfrag(cbuf(First{}), j);
+      read_scales(sbuf(First{}));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = CARRY; i < NR; ++i) carried[i] = 0.f;
+      rounds([&](auto which, int s) __attribute__((always_inline)) {
+        constexpr int k = decltype(which)::value;
+        using Next = std::integral_constant<int, k + 1>;
+        using Fill = std::integral_constant<int, k + BUFS - 1>;
+        stage(rbuf(which), rbuf(Next{}), cbuf(Next{}), sbuf(Next{}), rbuf(Fill{}), cbuf(Fill{}), sbuf(Fill{}), s + k);
+      });
+      tile_for<LAST - 3, LAST>([&](auto n) __attribute__((always_inline)) { add(n, carried); });
+    }
     wait_tile<0>();  // the last loads into LDS land before it is given back
   }
 
