@@ -23,7 +23,7 @@ inline BlockLaunch fp8_skinny_launch(int32_t n, int32_t G, bool grouped, int32_t
 // does without), fitted to 1 to 64 groups of 1 to 1024 rows of weights 1024 x 8192 to 5120 x 13824.  Of
 // groups only the mean size is known: each is taken to end in half a tile.
 // A step is 128 contracted elements.  Tiles of 64 take 0.52 us for a step while they leave CUs free, and
-// 0.0014 us a tile beyond; of 128, 0.95 and 0.0037; of 256, 1.9 us a round of the card.  All of them, 8 us
+// 0.0014 us a tile beyond; of 128, 0.95 and 0.0037; of 256, 1.9 us a round of the card.  All of them, 8 to 12 us
 // and the weights at 4.8 TB/s.  Streaming takes 0.2 to 0.4 us, by rows, for a million weights and row
 // tile of 32, and 5 us and 1.1 to 1.9 for 1024 contracted elements at least.
 // Measured, us:                          streaming   64 x 64   128 x 128   256 x 256
@@ -47,7 +47,7 @@ inline BlockLaunch fp8_launch(bool dx, int32_t n, int32_t G, bool grouped, int32
   const auto tiles = [&](int B) { return row_tiles(B) * static_cast<double>(tiles_of(out, B)); };
   const double t64 = steps * std::max(0.52, 0.0014 * tiles(64)), t128 = steps * std::max(0.95, 0.0037 * tiles(128)),
                t256 = steps * 1.9 * std::max(1.0, std::ceil(tiles(256) / kCus - 0.1));
-  const double tiled = std::max(5 + std::min({t64, t128, t256}), 8 + met * million / 4.8);
+  const double tiled = std::max(5 + std::min({t64, t128, t256}), 8 + std::min(4.0, 0.06 * met * million) + met * million / 4.8);
   if (!dx) {
     const double one = mean <= 32 ? 0.2 + 0.0065 * mean : 0.36;
     if (5 + std::max((mean <= 16 ? 0.0011 : 0.0019) * h_in, row_tiles(32) * million * one) < tiled)

@@ -15,6 +15,7 @@ to 2^(2 (e + 2) - 13) = 2^(2 e - 9).  Those ("narrow") values are held to the fl
 import numpy as np
 import pytest
 
+import block_sizes
 from oracle import block_oracle as B
 from oracle import grouped_oracle as G
 
@@ -278,6 +279,18 @@ def test_grouped(torch, size, dtype, pad):
     check(torch, T, share, E, K, N, dtype, seed=E, pad=pad, narrow=True)
 
 
+@pytest.mark.parametrize("dx,size,form", list(block_sizes.cases()), ids=lambda v: str(v))
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_form(torch, dx, size, form, dtype):
+    """Each kernel form at sizes that test_block_forms.py checks to take it."""
+    T, share, E, depth, out = size
+    K, N = (out, depth) if dx else (depth, out)
+    rows_of, share = (T * share, 1) if dx else (T, share)
+    for narrow in (True, False):
+        check(torch, rows_of, share, max(E, 1), K, N, dtype, seed=T, pad=8 * narrow, grouped=E > 0, forward=not dx, dx=dx,
+              narrow=narrow)
+
+
 @pytest.mark.parametrize("ids", [[-1] * 40, [2] * 40, [0, 1, 2, 3] * 10, [5] + [-1] * 38 + [0], [3] * 39 + [7]], ids=str)
 def test_who_is_where(torch, ids):
     """No row of any group, one group alone, groups of one row."""
@@ -290,7 +303,7 @@ def test_every_column_and_block(torch):
     """One row of ones against a weight whose elements tell where they are: each block has a scale of its own."""
     import adapter_gemv_amd as sgmv
     K, N = 400, 656
-    for T in (1, 40, 300):
+    for T in (1, 40, 300, 3000, 9000):
         for at in (0, 127, 128, 200, 384, 399):
             x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
             x[:, at] = 1.0
@@ -306,7 +319,7 @@ def test_every_column_and_block(torch):
             assert torch.equal(dx, scales[at // 128, torch.arange(K, device="cuda") // 128].to(dx.dtype).expand(T, K))
 
 
-@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("T", [3, 40, 300, 3000, 9000])
 def test_what_is_not_finite_stays_where_it_is(torch, T):
     """NaN codes, NaN and infinite scales, and rows that hold an infinity: their rows and columns, and no others."""
     import adapter_gemv_amd as sgmv
