@@ -46,7 +46,8 @@ __device__ inline uint32_t block_top(uint32_t top) {
 // Rows: 16 lanes to a block, 8 elements each; a wavefront takes four blocks of a row.
 struct Fp8Rows {
   int64_t rows, ld;
-  int32_t h, units;  // units of 512 elements of a row
+  int32_t h, pitch;  // of the codes: h, or h and zeros up to a multiple of 16
+  int32_t units;     // of 512 elements of a row
 };
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(uint8_t* __restrict__ codes, float* __restrict__ scales,
@@ -58,8 +59,9 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(uint8_t* __restrict__
   const bool in = at < R.h;
   const uint4 v = in ? ld16(x + row * R.ld + at) : zero4();
   const float s = block_scale<DT>(block_top(top_of(v)));
+  if (at >= R.pitch) return;
+  *reinterpret_cast<u32x2_t*>(codes + row * R.pitch + at) = encode8_finite<DT>(v, s);
   if (!in) return;
-  *reinterpret_cast<u32x2_t*>(codes + row * R.h + at) = encode8_finite<DT>(v, s);
   if (at % kBlock == 0) scales[row * blocks_of(R.h) + at / kBlock] = s;
 }
 
@@ -147,7 +149,7 @@ hipError_t launch_fp8(hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
 template <bool DX>
 hipError_t launch_fp8(int32_t dtype, hipStream_t s, const Fp8Args& A, const BlockLaunch& L) {
   const int32_t depth = DX ? A.h_out : A.h_in;
-  const bool near = depth % 128 == 0 && static_cast<int64_t>(shared_rows(A.T.n, A.share_rows)) * depth <= UINT32_MAX &&
+  const bool near = depth % 128 == 0 && static_cast<int64_t>(shared_rows(A.T.n, A.share_rows)) * A.ld_r <= UINT32_MAX &&
                     static_cast<int64_t>(A.h_in) * A.h_out <= UINT32_MAX;
   if (near) return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX, true>(s, A, L) : launch_fp8<SGMV_BF16, DX, true>(s, A, L);
   return dtype == SGMV_F16 ? launch_fp8<SGMV_F16, DX, false>(s, A, L) : launch_fp8<SGMV_BF16, DX, false>(s, A, L);
@@ -170,17 +172,27 @@ hipError_t launch_fp8_skinny(int32_t dtype, hipStream_t s, const Fp8Args& A, con
 // ------------------------------------------------------------------------------------
 constexpr int64_t kMostGroups = (int64_t(1) << 24) - 1;  // workgroups of 256 threads in a grid
 
-inline int check_fp8_dim(int32_t h) {
-  if (h < 16 || h > kMaxDim) return SGMV_ERR_SHAPE;
-  return h % 16 != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
+inline int check_fp8_dim(int32_t h, int unit = 16) {
+  if (h < unit || h > kMaxDim) return SGMV_ERR_SHAPE;
+  return h % unit != 0 ? SGMV_ERR_ALIGNMENT : SGMV_OK;
+}
+// of a weight: its rows are whole pieces
+inline int check_fp8_dims(int32_t h_in, int32_t h_out) {
+  if (int st = check_fp8_dim(h_in)) return st;
+  return check_fp8_dim(h_out, 8);
+}
+
+// 16-bit rows that a launch of the quantiser takes
+inline int check_rows16(int64_t rows, int32_t h, int64_t ld) {
+  if (ld < h) return SGMV_ERR_SHAPE;
+  if (ld % 8 != 0) return SGMV_ERR_ALIGNMENT;
+  return rows < 0 || rows > kMostGroups * 4 / ((h + 511) / 512) ? SGMV_ERR_SHAPE : SGMV_OK;
 }
 
 inline int check_fp8_rows(int32_t dtype, int64_t rows, int32_t h, int64_t ld) {
   if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
   if (int st = check_fp8_dim(h)) return st;
-  if (ld < h) return SGMV_ERR_SHAPE;
-  if (ld % 8 != 0) return SGMV_ERR_ALIGNMENT;
-  return rows < 0 || rows > kMostGroups * 4 / ((h + 511) / 512) ? SGMV_ERR_SHAPE : SGMV_OK;
+  return check_rows16(rows, h, ld);
 }
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -193,7 +205,8 @@ inline size_t weight_scales(int32_t G, int32_t h_in, int32_t h_out) {
   return 4 * static_cast<size_t>(G) * blocks_of(h_in) * blocks_of(h_out);
 }
 
-inline Fp8Rows fp8_rows(int64_t rows, int32_t h, int64_t ld) { return {rows, ld, h, (h + 511) / 512}; }
+inline Fp8Rows fp8_rows(int64_t rows, int32_t h, int64_t ld, int32_t pitch) { return {rows, ld, h, pitch, (h + 511) / 512}; }
+inline int32_t pitch_of(int32_t h) { return (h + 15) / 16 * 16; }
 inline uint32_t fp8_grid(const Fp8Rows& R) { return static_cast<uint32_t>((R.rows * R.units + 3) / 4); }
 
 hipError_t launch_quantize(int32_t dtype, hipStream_t s, void* codes, float* scales, const void* x, const Fp8Rows& R) {
@@ -206,8 +219,7 @@ hipError_t launch_quantize(int32_t dtype, hipStream_t s, void* codes, float* sca
 inline int check_fp8_weight(int32_t dtype, const void* W, int64_t stride, const void* codes, const void* scales,
                             int32_t G, int32_t h_in, int32_t h_out) {
   if (dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
-  int st;
-  if ((st = check_fp8_dim(h_in)) || (st = check_fp8_dim(h_out))) return st;
+  if (int st = check_fp8_dims(h_in, h_out)) return st;
   const int64_t elems = static_cast<int64_t>(h_in) * h_out;
   if (G < 1 || stride < elems || static_cast<int64_t>(blocks_of(h_in)) * blocks_of(h_out) > kMostGroups / G)
     return SGMV_ERR_SHAPE;
@@ -233,7 +245,7 @@ extern "C" int sgmv_block_quantize(hipStream_t stream, int32_t dtype, void* code
   if (ranges_overlap(codes, c, x, xb) || ranges_overlap(scales, s, x, xb) || ranges_overlap(codes, c, scales, s))
     return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
-  return hip_status(launch_quantize(dtype, stream, codes, scales, x, fp8_rows(rows, h, ld_x)));
+  return hip_status(launch_quantize(dtype, stream, codes, scales, x, fp8_rows(rows, h, ld_x, h)));
 }
 
 extern "C" int sgmv_block_dequantize(hipStream_t stream, int32_t dtype, void* y, int64_t ld_y, const void* codes,
@@ -246,7 +258,7 @@ extern "C" int sgmv_block_dequantize(hipStream_t stream, int32_t dtype, void* y,
   if (ranges_overlap(codes, static_cast<size_t>(rows) * h, y, yb) || ranges_overlap(scales, row_scales(rows, h), y, yb))
     return SGMV_ERR_ALIAS;
   if (int st = check_device()) return st;
-  const Fp8Rows R = fp8_rows(rows, h, ld_y);
+  const Fp8Rows R = fp8_rows(rows, h, ld_y, h);
   const auto kernel = dtype == SGMV_F16 ? fp8_dequantize_kernel<SGMV_F16> : fp8_dequantize_kernel<SGMV_BF16>;
   kernel<<<fp8_grid(R), 256, 0, stream>>>(static_cast<uint16_t*>(y), static_cast<const uint8_t*>(codes), scales, R);
   return hip_status(hipGetLastError());
@@ -294,16 +306,16 @@ struct Product {
   int32_t rows() const { return shared_rows(n, share); }
 };
 
-inline size_t codes_room(int64_t rows, int32_t h) { return align_up(static_cast<size_t>(rows) * h, 256); }
+inline size_t codes_room(int64_t rows, int32_t h) { return align_up(static_cast<size_t>(rows) * pitch_of(h), 256); }
 inline size_t rows_room(int64_t rows, int32_t h) { return rows <= 0 ? 0 : codes_room(rows, h) + row_scales(rows, h); }
 
 int product(hipStream_t stream, const Product& P, bool quantized) {
   if (P.dtype != SGMV_F16 && P.dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
   int st;
-  if ((st = check_groups(P.n, P.G, P.share, P.starts, P.perm)) || (st = check_fp8_dim(P.h_in)) ||
-      (st = check_fp8_dim(P.h_out)) || (st = check_dim(P.cols(), P.ld_out)))
+  if ((st = check_groups(P.n, P.G, P.share, P.starts, P.perm)) || (st = check_fp8_dims(P.h_in, P.h_out)) ||
+      (st = check_dim(P.cols(), P.ld_out)) || (quantized && (st = check_fp8_dim(P.depth()))) ||
+      (!quantized && (st = check_rows16(P.rows(), P.depth(), P.ld_r))))
     return st;
-  if (!quantized && (st = check_fp8_rows(P.dtype, P.rows(), P.depth(), P.ld_r))) return st;
   const BlockLaunch L = fp8_launch(P.dx, P.n, P.G, P.starts, P.h_in, P.h_out);
   if (!L.fits()) return SGMV_ERR_SHAPE;
   if (P.n == 0) return SGMV_OK;
@@ -334,6 +346,7 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   A.T = {P.starts, P.perm, P.n, P.G};
   A.share = share_of(P.share);
   A.share_rows = P.share;
+  A.ld_r = pitch_of(P.depth());
   if (quantized) {
     A.r = static_cast<const uint8_t*>(P.r);
     A.r_scale = P.r_scales;
@@ -343,7 +356,7 @@ int product(hipStream_t stream, const Product& P, bool quantized) {
   } else {
     uint8_t* const codes = static_cast<uint8_t*>(P.workspace);
     float* const scales = reinterpret_cast<float*>(codes + codes_room(P.rows(), P.depth()));
-    if (hipError_t e = launch_quantize(P.dtype, stream, codes, scales, P.r, fp8_rows(P.rows(), P.depth(), P.ld_r)))
+    if (hipError_t e = launch_quantize(P.dtype, stream, codes, scales, P.r, fp8_rows(P.rows(), P.depth(), P.ld_r, pitch_of(P.depth()))))
       return hip_status(e);
     A.r = codes, A.r_scale = scales;
   }

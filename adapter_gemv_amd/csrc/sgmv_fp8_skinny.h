@@ -44,7 +44,7 @@ struct Fp8Skinny {
       if constexpr (X16) {
         xh[m] = global_ptr(A.x) + row * A.ld_x + 16 * kq;
       } else {
-        xp[m] = global_ptr(A.r) + row * K + 16 * kq;
+        xp[m] = global_ptr(A.r) + row * A.ld_r + 16 * kq;
         xs[m] = global_ptr(A.r_scale) + row * kb;
       }
 #pragma unroll

@@ -28,12 +28,12 @@ struct Fp8Args {
   RowTab T;
   Share share;
   const uint16_t* x;      // rows in 16 bits, ld_x elements apart, or
-  const uint8_t* r;       // rows of x or dy, dense
+  const uint8_t* r;       // rows of x or dy in 8 bits, ld_r apart, zeros up to a multiple of 16
   const float* r_scale;   // [rows, blocks]
   const uint8_t* w;       // [h_out, h_in]
   const float* w_scale;   // [blocks of h_out, blocks of h_in]
   uint16_t* out;
-  int64_t ld_x, ld_out;
+  int64_t ld_x, ld_r, ld_out;
   int32_t h_in, h_out;
   int32_t share_rows;     // rows that share one of r
 };
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * WR * WC, BUFS * BR >= 512 && BR < 256 ? 1 : 2)
     const int q = (w * RI + i) * 8 + lane / 8;
     rk[i] = 16 * ((lane & 7) ^ ((q >> 1) & 7));
     const int j = nst ? A.share.div(A.T.row(t.row0 + min(q, t.rows - 1))) : 0;
-    rp[i] = static_cast<Offset>(j) * depth + rk[i];
+    rp[i] = static_cast<Offset>(j) * static_cast<Offset>(A.ld_r) + rk[i];
   }
 #pragma unroll
   for (int i = 0; i < CI; ++i) {

@@ -110,8 +110,8 @@ def fp8_quantize(x, stream=None) -> Fp8Rows:
 
 
 def fp8_quantize_weight(W, stream=None) -> Fp8Weight:
-    """W [E, h_out, h_in] or [h_out, h_in] (float16 or bfloat16, multiples of 16) in 8 bits, one
-    scale for 128 x 128 elements."""
+    """W [E, h_out, h_in] or [h_out, h_in] (float16 or bfloat16, h_in a multiple of 16, h_out of 8) in
+    8 bits, one scale for 128 x 128 elements."""
     torch = _torch()
     E, h_out, h_in, stride = _weight_groups(W, "W")
     check_sizes("sgmv_block_quantize_weight", E, h_out, h_in)

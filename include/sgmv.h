@@ -614,11 +614,11 @@ int sgmv_combine_rows_backward(hipStream_t stream, int32_t dtype, void* dy, int6
 /*
  * 8-bit floating point with a scale for each block of 128 (the library's "block" format): one sign, four exponent and three
  * mantissa bits (0x00 .. 0x7e are 0, then 2^-9 up to 448; 0x7f is NaN; + 0x80 the negative), and
- * float32 scales of any value.  h is a multiple of 16 and need not be one of 128: the last block
- * is shorter.
- *   rows     codes uint8 [rows, h], scales float32 [rows, ceil(h / 128)]
+ * float32 scales of any value.
+ *   rows     codes uint8 [rows, h], scales float32 [rows, ceil(h / 128)], h a multiple of 16
  *   weights  codes uint8 [G, h_out, h_in], scales float32 [G, ceil(h_out / 128),
- *            ceil(h_in / 128)]: one for each 128 x 128
+ *            ceil(h_in / 128)]: one for each 128 x 128; h_in a multiple of 16, h_out of 8
+ * Sizes need not be multiples of 128: the last blocks are smaller.
  * all dense, codes 16-byte aligned.  An element is its code's value times its block's scale.
  *
  * The quantisers take 16-bit values (dtype).  A block's scale is the least power of two, not below
@@ -651,8 +651,8 @@ int sgmv_block_dequantize_weight(hipStream_t stream, int32_t dtype, void* W, int
  *
  * The products of a block are summed in float32, times the float32 product of its two scales
  * (which has to lie in float32's normal range, 2^-126 up to 2^128, to count in full).  The gradient
- * of the weights is sgmv_group_matmul_dw, of the 16-bit rows.  h_in and h_out are multiples of 16;
- * everything else is as for the 16-bit calls.
+ * of the weights is sgmv_group_matmul_dw, of the 16-bit rows.  h_in is a multiple of 16 (as is
+ * h_out where dy comes in 8 bits); everything else is as for the 16-bit calls.
  *   workspace  device memory, 16-byte aligned, of at least sgmv_block_workspace_bytes of the same
  *              sizes (0 for some: then it may be NULL), with any contents; its contents after the
  *              call are of no use.  It may not overlap any operand, and calls that share one must

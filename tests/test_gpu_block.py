@@ -93,7 +93,8 @@ def test_rows_and_back(torch, shape, dtype):
         assert torch.equal(back.cpu(), want)
 
 
-@pytest.mark.parametrize("shape", [(1, 16, 16), (1, 128, 128), (3, 144, 272), (2, 1040, 528), (1, 2048, 16), (5, 16, 400)],
+@pytest.mark.parametrize("shape", [(1, 16, 16), (1, 128, 128), (3, 144, 272), (2, 1040, 528), (1, 2048, 16), (5, 16, 400),
+                                   (3, 136, 272), (2, 8, 16)],
                          ids=str)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_weights_and_back(torch, shape, dtype):
@@ -250,8 +251,9 @@ def check(torch, T, share, E, K, N, dtype, seed=0, ids=None, pad=0, grouped=True
         d = sgmv.fp8_matmul_dx(out, dy, W, groups)
         assert d is out
         close(f64(d), ref, mag, N, dtype, what + " dx", narrow)
-        d8 = sgmv.fp8_matmul_dx(torch.full_like(d.contiguous(), float("nan")), sgmv.fp8_quantize(dy), W, groups)
-        assert torch.equal(d, d8)
+        if N % 16 == 0:
+            d8 = sgmv.fp8_matmul_dx(torch.full_like(d.contiguous(), float("nan")), sgmv.fp8_quantize(dy), W, groups)
+            assert torch.equal(d, d8)
 
 
 DENSE = [(1, 16, 16), (1, 128, 128), (1, 4096, 1024), (3, 144, 272), (16, 1040, 528), (17, 272, 144), (33, 2064, 400),
@@ -264,6 +266,20 @@ DENSE = [(1, 16, 16), (1, 128, 128), (1, 4096, 1024), (3, 144, 272), (16, 1040, 
 def test_dense(torch, size, dtype, narrow):
     T, K, N = size
     check(torch, T, 1, 1, K, N, dtype, seed=T, grouped=False, narrow=narrow)
+
+
+ODD = [(1, 1, 1, 16, 8), (5, 2, 3, 144, 136), (40, 1, 1, 272, 520), (300, 2, 2, 400, 264), (2100, 1, 3, 1040, 1032),
+       (2050, 1, 1, 640, 4104), (1111, 1, 1, 4112, 648)]
+
+
+@pytest.mark.parametrize("size", ODD, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_h_out_that_is_no_multiple_of_16(torch, size, dtype):
+    """Beside the last codes of dy lie zeros, whatever the workspace held."""
+    T, share, E, K, N = size
+    torch.full((1 << 26,), 0x7f, dtype=torch.uint8, device="cuda")  # what an allocation may get next: NaN
+    check(torch, T, share, E, K, N, dtype, seed=N, grouped=E > 1, pad=8)
+    check(torch, T, share, E, K, N, dtype, seed=N, grouped=E > 1, narrow=True)
 
 
 GROUPED = [(1, 2, 8, 512, 272), (5, 1, 3, 144, 400), (32, 2, 64, 272, 144), (40, 4, 5, 656, 528), (200, 2, 4, 1040, 272),

@@ -72,7 +72,8 @@ BAD = [
     (WEIGHTS, dict(scales=C), O), (WEIGHTS, dict(scales=A), O),
     (MULS, dict(dtype=2), U), (MULS, dict(n=-1), S), (MULS, dict(n=(1 << 30) + 1), S), (MULS, dict(G=0), S),
     (MULS, dict(G=1025), U), (MULS, dict(starts=None), N), (MULS, dict(perm=None), N), (MULS, dict(h_in=0), S),
-    (MULS, dict(h_in=248), L), (MULS, dict(h_out=520, ld_x=520, ld_y=520), L), (MULS, dict(ld_y=248), S),
+    (MULS, dict(h_in=248), L), (MULS, dict(h_out=516, ld_x=516, ld_y=516), L),
+    (MULS[3:], dict(h_out=520, ld_x=520), L), (WEIGHTS, dict(h_out=508), L), (MULS, dict(ld_y=248), S),
     (MULS, dict(ld_y=1028), L), (MULS, dict(y=None), N), (MULS, dict(x=None), N), (MULS, dict(w=None), N),
     (MULS, dict(ws=None), N), (MULS, dict(y=A + 8), L), (MULS, dict(x=B + 8), L), (MULS, dict(w=D + 8), L),
     (MULS, dict(ws=E + 2), L), (MULS, dict(y=B), O), (MULS, dict(y=D), O), (MULS, dict(y=D + 4 * 256 * 512 - 16), O),
@@ -125,6 +126,7 @@ def test_workspace_bytes():
     assert L.sgmv_block_dx_workspace_bytes(0, 256) == 0
     # codes, rounded up to 256, and a scale for each block that was begun
     assert L.sgmv_block_dx_workspace_bytes(100, 272) == (100 * 272 + 255) // 256 * 256 + 100 * 3 * 4
+    assert L.sgmv_block_dx_workspace_bytes(100, 264) == (100 * 272 + 255) // 256 * 256 + 100 * 3 * 4
     assert L.sgmv_block_workspace_bytes(8192, 4, 1, 0, 2048, 2048) == 2048 * 2048 + 2048 * 16 * 4
     assert L.sgmv_block_dx_workspace_bytes(1 << 30, 1 << 22) == (1 << 52) + (1 << 30) * (1 << 15) * 4
 
