@@ -16,9 +16,9 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check, check_sizes
-from .grouped import RowGroups, _empty, _ld, _share, _stream_of, _tables
+from .grouped import RowGroups, _empty, _matrix, _share, _stream_of, _tables
 from .mx import _as_rows
-from .sgmv import _check_rows, _torch, dtype_code
+from .sgmv import _torch, dtype_code
 
 BLOCK = 128
 
@@ -150,8 +150,7 @@ def fp8_dequantize(y, q, stream=None):
 
 def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: bool):
     where = "sgmv_block_matmul_dx" if dx else "sgmv_block_matmul"
-    n = out.shape[0]
-    _check_rows(out, n, "dx" if dx else "y")
+    n, out_cols, ld_out = _matrix(out, "dx" if dx else "y")
     E = 1 if groups is None else groups.n_groups
     codes, scales = W.codes, W.scales
     shape = codes.shape
@@ -160,8 +159,13 @@ def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: b
         raise ValueError(f"W must be [{E}, h_out, h_in]")
     depth, cols = (h_out, h_in) if dx else (h_in, h_out)
     eight = isinstance(rows, Fp8Rows)
-    rs = rows.shape
-    if len(rs) != 2 or rs[1] != depth or out.shape[1] != cols:
+    if eight:
+        rs = rows.codes.shape
+        if len(rs) != 2:
+            raise ValueError("rows in 8 bits must be [n, h]")
+    else:
+        *rs, ld = _matrix(rows, "dy" if dx else "x")
+    if rs[1] != depth or out_cols != cols:
         raise ValueError(f"rows {tuple(rs)} and output {tuple(out.shape)} do not match W's h_in = {h_in}, "
                          f"h_out = {h_out}")
     if dx and rs[0] != n:
@@ -173,13 +177,12 @@ def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: b
     tail = (codes.data_ptr(), scales.data_ptr(), starts, perm, n, E, h_in, h_out)
     if eight:
         handle = _stream_of(stream, out, rows.codes, rows.scales, codes, scales)
-        head = (handle, dt, out.data_ptr(), _ld(out), rows.codes.data_ptr(), rows.scales.data_ptr())
+        head = (handle, dt, out.data_ptr(), ld_out, rows.codes.data_ptr(), rows.scales.data_ptr())
         st = (lib.sgmv_block_matmul_dx_quantized(*head, *tail) if dx else
               lib.sgmv_block_matmul_quantized(*head, share, *tail))
         check(st, where + "_quantized")
         return out
-    _check_rows(rows, rs[0], "dy" if dx else "x")
-    if rows.dtype != out.dtype:
+    if rows.dtype is not out.dtype:
         raise TypeError("the rows and the output must share a dtype")
     handle = _stream_of(stream, out, rows, codes, scales)
     room = (lib.sgmv_block_dx_workspace_bytes(n, h_out) if dx else
@@ -188,7 +191,7 @@ def _product(out, rows, W: Fp8Weight, groups: Optional[RowGroups], stream, dx: b
     if room:
         space = _empty(out, (room,), _torch().uint8, stream)
         at = space.data_ptr()
-    head = (handle, dt, out.data_ptr(), _ld(out), rows.data_ptr(), _ld(rows))
+    head = (handle, dt, out.data_ptr(), ld_out, rows.data_ptr(), ld)
     st = (lib.sgmv_block_matmul_dx(*head, *tail, at, room) if dx else
           lib.sgmv_block_matmul(*head, share, *tail, at, room))
     check(st, where)

@@ -121,6 +121,15 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+def _matrix(t, name: str):
+    """(rows, columns, elements between rows) of a matrix."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or strides[1] != 1:
+        raise ValueError(f"{name} must be [n, h] with unit column stride")
+    n, h = shape
+    return n, h, strides[0] if n > 1 else h
+
+
 def _pool(W, groups: Optional[RowGroups], name: str):
     """A weight [E, h_out, h_in] (or [h_out, h_in] without groups): (h_out, h_in, stride)."""
     E = 1 if groups is None else groups.n_groups

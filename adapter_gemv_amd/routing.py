@@ -21,8 +21,8 @@ from typing import Optional
 
 from . import _lib
 from ._lib import check, check_sizes
-from .grouped import _empty, _ld, _stream_of
-from .sgmv import _check_rows, _torch, dtype_code
+from .grouped import _empty, _matrix, _stream_of
+from .sgmv import _torch, dtype_code
 
 SCORES = {"softmax": _lib.SOFTMAX, "sigmoid": _lib.SIGMOID}
 
@@ -38,10 +38,17 @@ class Routes:
     scale: float = 1.0
 
 
-def _logits_code(t, name: str) -> int:
-    if t.dim() != 2 or not t.is_contiguous() and t.stride(1) != 1 and t.shape[1] > 1 or t.shape[1] == 0:
-        raise ValueError(f"{name} must be [T, E] with unit column stride")
-    return _lib.F32 if t.dtype is _torch().float32 else dtype_code(t)
+def _logits(t, name: str):
+    """(T, E, elements between rows, dtype) of logits."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] == 0:
+        raise ValueError(f"{name} must be [T, E]")
+    dt = _lib.F32 if t.dtype is _torch().float32 else dtype_code(t)
+    T, E = shape
+    row, column = t.stride()
+    if column != 1 and E > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return T, E, row if T > 1 else E, dt
 
 
 def _scores_code(scores: str) -> int:
@@ -66,8 +73,7 @@ def route(logits, k: int, *, bias=None, scores: str = "softmax", expert_groups: 
     the scores, divided by the sum of the chosen ones with ``normalize``.  A token whose logits are all
     minus infinity gets ids -1 and weights 0."""
     torch = _torch()
-    dt, code = _logits_code(logits, "logits"), _scores_code(scores)
-    T, E = logits.shape
+    (T, E, ld, dt), code = _logits(logits, "logits"), _scores_code(scores)
     keep = expert_groups if keep_groups is None else keep_groups
     check_sizes("sgmv_route", T, E, k, expert_groups, keep, group_best)
     if k < 1 or k > E:
@@ -80,7 +86,7 @@ def route(logits, k: int, *, bias=None, scores: str = "softmax", expert_groups: 
     ids = _empty(logits, (T, k), torch.int32, stream)
     weights = _empty(logits, (T, k), torch.float32, stream)
     st = _lib.lib().sgmv_route(handle, dt, ids.data_ptr(), weights.data_ptr(), logits.data_ptr(),
-                               _ld(logits), None if bias is None else bias.data_ptr(), T, E, k,
+                               ld, None if bias is None else bias.data_ptr(), T, E, k,
                                expert_groups, keep, group_best, code, bool(normalize), scale)
     check(st, "sgmv_route")
     return Routes(ids, weights, scores, bool(normalize), float(scale))
@@ -90,11 +96,11 @@ def route_backward(dlogits, dweights, logits, routes: Routes, stream=None):
     """Write the gradient of the logits into ``dlogits`` (their shape and type) from that of the
     weights (float32 [T, k]); the choice of experts is held fixed."""
     torch = _torch()
-    dt, code = _logits_code(logits, "logits"), _scores_code(routes.scores)
-    if _logits_code(dlogits, "dlogits") != dt:
+    (T, E, ld, dt), code = _logits(logits, "logits"), _scores_code(routes.scores)
+    dT, dE, ld_d, ddt = _logits(dlogits, "dlogits")
+    if ddt != dt:
         raise TypeError("logits and dlogits must share a dtype")
-    T, E = logits.shape
-    if tuple(dlogits.shape) != (T, E):
+    if dT != T or dE != E:
         raise ValueError(f"dlogits {tuple(dlogits.shape)} does not match logits [{T}, {E}]")
     ids = routes.ids
     if ids.dim() != 2:
@@ -104,44 +110,42 @@ def route_backward(dlogits, dweights, logits, routes: Routes, stream=None):
     _dense(dweights, torch.float32, (T, k), "dweights")
     check_sizes("sgmv_route_backward", T, E)
     handle = _stream_of(stream, dlogits, dweights, logits, ids)
-    st = _lib.lib().sgmv_route_backward(handle, dt, dlogits.data_ptr(), _ld(dlogits), dweights.data_ptr(),
-                                        logits.data_ptr(), _ld(logits), ids.data_ptr(), T, E, k, code,
+    st = _lib.lib().sgmv_route_backward(handle, dt, dlogits.data_ptr(), ld_d, dweights.data_ptr(),
+                                        logits.data_ptr(), ld, ids.data_ptr(), T, E, k, code,
                                         bool(routes.normalize), routes.scale)
     check(st, "sgmv_route_backward")
     return dlogits
 
 
 def _tokens(out, y, weights, what: str):
-    """(T, k, h, dtype) of a call whose rows are y [T * k, h] and whose tokens are out [T, h]."""
-    if out.dim() != 2 or y.dim() != 2:
-        raise ValueError(f"{what} and the experts' rows must be matrices")
-    (T, h), (n, width) = out.shape, y.shape
-    _check_rows(out, T, what)
-    _check_rows(y, n, "the experts' rows")
+    """(T, k, h, dtype, strides of out and y) of a call whose rows are y [T * k, h] and whose tokens are
+    out [T, h]."""
+    T, h, ld_out = _matrix(out, what)
+    n, width, ld_y = _matrix(y, "the experts' rows")
     if width != h:
         raise ValueError(f"{what} [., {h}] and the experts' rows [., {width}] do not match")
     if out.dtype is not y.dtype:
         raise TypeError("all rows must share a dtype")
     k = n // T if T else 1
     if weights is not None:
-        if weights.dim() != 2:
-            raise ValueError(f"weights must be [{T}, k]")
-        if not T:
+        if not T and weights.dim() == 2:
             k = weights.shape[1]
         _dense(weights, _torch().float32, (T, k), "weights")
     if n != T * k or k < 1:
         raise ValueError(f"{n} rows are not the experts' of {T} tokens")
     check_sizes("sgmv_combine_rows", n, k, h)
-    return T, k, h, dtype_code(y)
+    return T, k, h, dtype_code(y), ld_out, ld_y
 
 
 def combine_rows(out, y, weights=None, add: bool = False, stream=None):
     """out[t] = sum over j of weights[t, j] * y[t * k + j] (plus what out holds, with ``add``);
     without weights their plain sum.  out [T, h], y [T * k, h], weights float32 [T, k]."""
-    T, k, h, dt = _tokens(out, y, weights, "out")
-    handle = _stream_of(stream, out, y) if weights is None else _stream_of(stream, out, y, weights)
-    st = _lib.lib().sgmv_combine_rows(handle, dt, out.data_ptr(), _ld(out), y.data_ptr(), _ld(y),
-                                      None if weights is None else weights.data_ptr(), T, k, h, bool(add))
+    T, k, h, dt, ld_out, ld_y = _tokens(out, y, weights, "out")
+    if weights is None:
+        handle, at = _stream_of(stream, out, y), None
+    else:
+        handle, at = _stream_of(stream, out, y, weights), weights.data_ptr()
+    st = _lib.lib().sgmv_combine_rows(handle, dt, out.data_ptr(), ld_out, y.data_ptr(), ld_y, at, T, k, h, bool(add))
     check(st, "sgmv_combine_rows")
     return out
 
@@ -149,23 +153,23 @@ def combine_rows(out, y, weights=None, add: bool = False, stream=None):
 def combine_rows_backward(dy, dweights, dout, y=None, weights=None, stream=None):
     """dy[t * k + j] = weights[t, j] * dout[t] and dweights[t, j] = dout[t] . y[t * k + j]; without
     weights (then dweights and y are None) dout's rows alone, k times each."""
-    T, k, h, dt = _tokens(dout, dy, weights, "dout")
+    T, k, h, dt, ld_dout, ld_dy = _tokens(dout, dy, weights, "dout")
     if weights is None:
         if dweights is not None:
             raise ValueError("dweights without weights")
         handle = _stream_of(stream, dy, dout)
-        st = _lib.lib().sgmv_combine_rows_backward(handle, dt, dy.data_ptr(), _ld(dy), None, dout.data_ptr(),
-                                                   _ld(dout), None, 0, None, T, k, h)
+        st = _lib.lib().sgmv_combine_rows_backward(handle, dt, dy.data_ptr(), ld_dy, None, dout.data_ptr(), ld_dout,
+                                                   None, 0, None, T, k, h)
     else:
         _dense(dweights, _torch().float32, (T, k), "dweights")
-        _check_rows(y, T * k, "y")
-        if y.shape[1] != h:
-            raise ValueError(f"y [., {y.shape[1]}] does not match dout [., {h}]")
-        if y.dtype != dy.dtype:
+        n, width, ld_y = _matrix(y, "y")
+        if n != T * k or width != h:
+            raise ValueError(f"y [{n}, {width}] does not match dy [{T * k}, {h}]")
+        if y.dtype is not dy.dtype:
             raise TypeError("all rows must share a dtype")
         handle = _stream_of(stream, dy, dweights, dout, y, weights)
-        st = _lib.lib().sgmv_combine_rows_backward(handle, dt, dy.data_ptr(), _ld(dy), dweights.data_ptr(),
-                                                   dout.data_ptr(), _ld(dout), y.data_ptr(), _ld(y),
-                                                   weights.data_ptr(), T, k, h)
+        st = _lib.lib().sgmv_combine_rows_backward(handle, dt, dy.data_ptr(), ld_dy, dweights.data_ptr(),
+                                                   dout.data_ptr(), ld_dout, y.data_ptr(), ld_y, weights.data_ptr(),
+                                                   T, k, h)
     check(st, "sgmv_combine_rows_backward")
     return dy, dweights
