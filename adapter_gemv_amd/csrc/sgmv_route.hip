@@ -110,6 +110,11 @@ __device__ inline T share_of_choice(T l, T top) {
   else return l >= 0 ? 1 / (1 + exp(-l)) : exp(l - (top < 0 ? top : T(0))) / (1 + exp(l));
 }
 
+// the value that chooses an expert by its sigmoid
+__device__ inline double exact_sigmoid(const RouteArgs& A, float l, int e) {
+  return 1 / (1 + exp(-static_cast<double>(l))) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0);
+}
+
 // One token by the whole wavefront, with the values that choose in 64 bits: for tokens whose choice
 // float32 leaves open, and for NaN.
 template <int N>
@@ -144,7 +149,8 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& A, int dtype, int
   for (int e = lane; e < A.E; e += 64) {
     const float l = logit(dtype, A.logits, at + e);
     const double c = by_logit ? (!SIGMOID && bad ? __builtin_nan("") : static_cast<double>(l))
-                              : score(l) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0);
+                     : SIGMOID ? exact_sigmoid(A, l, e)
+                               : score(l) + (A.bias ? static_cast<double>(A.bias[e]) : 0.0);
     S.key[e] = l == -kInf || c == -__builtin_inf() ? 0 : order(c);
     S.val[e] = c;
   }
@@ -215,9 +221,12 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& A, int dtype, int
 // tokens of a wavefront, against 30 for one token with 64 lanes and 4 experts each.
 //
 // What chooses: where nothing is added to a score, the logits, which order like it.  Otherwise c in
-// float32, with the least distance at which two of its values are sure to be in order; a token with
-// closer ones (among its first k + 1, or about groups) is done again in 64 bits, as is one with NaN.
-// Logits of 16384 tokens over 256 experts in 8 groups: see the table of times.
+// float32, with the least distance at which two of its values are sure to be in order.  Where closer ones
+// stand among a token's first k + 1, or close sums of groups, sigmoids are taken again in 64 bits for
+// these alone (the chosen ones and the next, each in its lane; the two best of each group); a token for
+// which that is not enough, one with NaN, and a softmax, whose sum takes all experts, are done again
+// by route_exactly.  A few of 16384 tokens have such values, and their wavefront is the last to end:
+// 16384 tokens, 256 experts in 8 groups, all redone by route_exactly 25 us, so 18.6; 128 experts, 13.4 and 10.4.
 //
 // Distances: a sigmoid's float32 value is off by at most 2^-22 (its exponential by (|l| + 1) 2^-23 of
 // itself, which the slope s (1 - s) takes to at most 0.48 * 2^-23; sum, reciprocal and the addition of
@@ -331,6 +340,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
     }
     __syncthreads();
     uint64_t kept = 0;
+    bool close = false;  // a group on the other side of the cut may be the better one
     for (int first = 0; first < A.groups; first += L) {
       const int g = first + l0;
       bool stay = false;
@@ -343,11 +353,44 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
           if (h != g && fabsf(other - mine) <= d && mine > -kInf && !by_logit) ++after;
         }
         stay = before < A.keep;
-        // a close one on the other side of the cut
-        if (after && before + after >= A.keep && before - after < A.keep) open = true;
+        close |= after && before + after >= A.keep && before - after < A.keep;
       }
       const uint64_t set = __ballot(stay);
       kept |= (L == 64 ? set : set >> (lane & 48) & 0xffffu) << first;
+    }
+    if (!SIGMOID || A.groups > L) {
+      open |= close;
+    } else if (__any(close)) {  // the scores in 64 bits, if it is plain which experts make them up
+      double score = -__builtin_inf();
+      if (l0 < A.groups) {
+        float b[3] = {-kInf, -kInf, -kInf};
+        int e0 = 0, e1 = 0;
+#pragma unroll 8
+        for (int i = 0; i < per; ++i) {
+          const float x = row[l0 * (per + 1) + i];
+          const int e = l0 * per + i;
+          const bool first = x > b[0], second = x > b[1];
+          b[2] = fmaxf(b[2], fminf(b[1], x));
+          e1 = first ? e0 : second ? e : e1;
+          b[1] = first ? b[0] : second ? x : b[1];
+          e0 = first ? e : e0;
+          b[0] = first ? x : b[0];
+        }
+        const bool two = A.best > 1 && b[1] > -kInf;
+        const float least = two ? b[1] : b[0], other = A.best > 1 ? b[2] : b[1];
+        open |= other > -kInf && !(least - other > apart(least));
+        if (b[0] > -kInf) {
+          score = exact_sigmoid(A, logit(dtype, A.logits, t * A.ld + e0), e0);
+          if (two) score += exact_sigmoid(A, logit(dtype, A.logits, t * A.ld + e1), e1);
+        }
+      }
+      int before = 0;
+      for (int h = 0; h < A.groups; ++h) {
+        const double other = __shfl(score, lane - l0 + h);
+        before += other > score || (other == score && h < l0);
+      }
+      const uint64_t set = __ballot(l0 < A.groups && before < A.keep);
+      kept = L == 64 ? set : set >> (lane & 48) & 0xffffu;
     }
 #pragma unroll
     for (int v = 0, g = g0, in = in0; v < V; ++v) {
@@ -362,18 +405,13 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
   for (int v = 0; v < V; ++v) key[v] = order(c[v]);
   int mine = -1;  // lane j of a token: its j-th expert
   uint32_t last = 0;
-  for (int j = 0; j < A.k + !by_logit; ++j) {
+  const auto most = [&] {
     uint32_t best = key[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) best = max(best, key[v]);
-    const uint32_t m = token_most<L>(best);
-    if (!by_logit && j > 0 && m) {
-      // back to the values that the keys stand for
-      const auto value = [](uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); };
-      open |= !(value(last) - value(m) > apart(value(last)));
-    }
-    last = m;
-    if (j == A.k) break;
+    return best;
+  };
+  const auto take = [&](int j, uint32_t best, uint32_t m) {  // the first of the lanes that have the largest
     const uint64_t set = __ballot(best == m);
     const int first = __builtin_ctzll(L == 64 ? set : set >> (lane & 48) & 0xffffu);
     int v0 = 0;
@@ -385,6 +423,40 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
     const int leaves = l0 == first ? v0 : V;
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = v == leaves ? 0u : key[v];
+  };
+  // whether the values that two keys stand for may be in another order
+  const auto near_keys = [&](uint32_t more, uint32_t less) {
+    const auto value = [](uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); };
+    return less && !(value(more) - value(less) > apart(value(more)));
+  };
+  bool close = false;
+  for (int j = 0; j < A.k; ++j) {
+    const uint32_t best = most(), m = token_most<L>(best);
+    if (!by_logit && j > 0) close |= near_keys(last, m);
+    last = m;
+    take(j, best, m);
+  }
+  if (!by_logit) {
+    const uint32_t best = most(), next = token_most<L>(best);  // of those that are left
+    const bool edge = near_keys(last, next);
+    if (!SIGMOID) {
+      open |= close || edge;
+    } else if (__any(close || edge)) {
+      // the chosen ones and the next in 64 bits, unless there are more that may belong to them
+      take(A.k, best, next);
+      const bool more = near_keys(last, token_most<L>(most()));  // by all lanes
+      open |= edge && (A.k == L || more);
+      const double c = mine < 0 ? 0 : exact_sigmoid(A, logit(dtype, A.logits, t * A.ld + mine), mine);
+      int rank = 0;
+      for (int h = 0; h < min(A.k + 1, L); ++h) {
+        const double other = __shfl(c, lane - l0 + h);
+        const int id = __shfl(mine, lane - l0 + h);
+        rank += id >= 0 && (other > c || (other == c && id < mine));
+      }
+      if (mine < 0) rank = l0;
+      mine = __builtin_amdgcn_ds_permute(4 * (lane - l0 + rank), mine);
+      if (l0 >= A.k) mine = -1;
+    }
   }
 
   const int64_t to = static_cast<int64_t>(t) * A.k + l0;

@@ -151,6 +151,34 @@ def test_values_next_to_each_other(torch, scores):
 
 
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,keep", [(32, 5, 1, 1), (256, 8, 1, 1), (250, 15, 1, 1), (256, 16, 1, 1),
+                                             (512, 20, 1, 1), (1024, 64, 1, 1), (64, 6, 8, 3), (256, 8, 8, 4),
+                                             (256, 9, 32, 5), (512, 30, 16, 7)])
+def test_pairs_that_float32_leaves_open(torch, scores, E, k, groups, keep):
+    """Values far from each other but for pairs a step apart or equal: inside the choice, across its end,
+    and among the sums of groups, of which each two hold the same values up to a step."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + k)
+    T, half = 96, E // 2
+
+    def order(*shape):
+        return torch.rand(*shape, generator=gen, device="cuda").argsort(-1)
+
+    a = order(T, half).float() * (3.0 / half) - 1.5
+    up = torch.nextafter(a, torch.full_like(a, 9.0))
+    b = torch.where(torch.rand(T, half, generator=gen, device="cuda") < 0.5, a, up)
+    if groups == 1:
+        logits = torch.cat([a, b], 1).gather(1, order(T, E))
+    else:
+        per = E // groups
+        pairs = torch.stack([a.view(T, groups // 2, per), b.view(T, groups // 2, per)], 2)
+        logits = pairs.view(T, groups, per).gather(2, order(T, groups, per)).view(T, E)
+    for bias in (None, torch.zeros(E, device="cuda"), torch.full((E,), 0.375, device="cuda")):
+        for best in (1, 2):
+            check(torch, logits, k, f"{E} {k} {scores} best {best}", bias, scores, groups, keep, best)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,k,groups,keep", [(9, 4, 3, 2), (64, 8, 1, 1), (256, 8, 8, 4), (1024, 20, 4, 1)])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_masks(torch, scores, E, k, groups, keep, normalize):
