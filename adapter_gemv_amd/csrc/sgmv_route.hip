@@ -649,6 +649,7 @@ void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, 
   const integral_constant<int, 64> all{};
   if (A.k > 16 || A.E > 256) {
     if (A.E <= 256) go(all, integral_constant<int, 4>{});
+    else if (A.E <= 512) go(all, integral_constant<int, 8>{});
     else go(all, integral_constant<int, 16>{});
   } else if (A.E <= 32) go(some, integral_constant<int, 2>{});
   else if (A.E <= 64) go(some, integral_constant<int, 4>{});
