@@ -229,9 +229,11 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& A, int dtype, int
 // 16384 tokens, 256 experts in 8 groups, all redone by route_exactly 25 us, so 18.6; 128 experts, 13.4 and 10.4.
 //
 // Distances: a sigmoid's float32 value is off by at most 2^-22 (its exponential by (|l| + 1) 2^-23 of
-// itself, which the slope s (1 - s) takes to at most 0.48 * 2^-23; sum, reciprocal and the addition of
-// the bias 2.5 * 2^-24), a softmax's by 2^-20 of the row's largest, most of it from the sum, and c by
-// 2^-24 of itself.  Twice that between two values, twice again for the sums of two; all of it doubled.
+// itself, which the slope s (1 - s) takes to at most 0.48 * 2^-23; sum and reciprocal 2.5 * 2^-24), a
+// softmax's by 2^-20 of the row's largest, most of it from the sum, and c by 2^-24 of itself.  Twice that
+// between two values; all of it doubled.  A group's sum is off by what its two values are (by 2^-24 of each
+// one's own size, which the sum need not have: biases of opposite sign cancel) and by 2^-24 of itself:
+// between two sums that of both groups, doubled, is twice a value's distance and 2^-22 of the sizes.
 template <int L, int V, bool SIGMOID, bool GROUPS>
 __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool normalize, bool vectors,
                                                    bool bias_vectors) {
@@ -336,7 +338,12 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
         b1 = fmaxf(b1, fminf(b0, x));
         b0 = fmaxf(b0, x);
       }
-      S.g.score[slot][g] = A.best > 1 && b1 > -kInf ? b0 + b1 : b0;
+      const bool two = A.best > 1 && b1 > -kInf;
+      S.g.score[slot][g] = two ? b0 + b1 : b0;
+      // in the place after the group: how far from its exact sum this score may be, doubled; minus infinity,
+      // which no distance is below, for logits and for infinities
+      const float size = fabsf(b0) + (two ? fabsf(b1) : 0.f);
+      row[g * (per + 1) + per] = by_logit || size == kInf ? -kInf : near + 0x1p-22f * size;
     }
     __syncthreads();
     uint64_t kept = 0;
@@ -345,13 +352,14 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
       const int g = first + l0;
       bool stay = false;
       if (g < A.groups) {
-        const float mine = S.g.score[slot][g], d = 2 * apart(mine);
+        const float mine = S.g.score[slot][g], off = row[g * (per + 1) + per];
         int before = 0, after = 0;  // surely better ones, and those that may be
         for (int h = 0; h < A.groups; ++h) {
           const float other = S.g.score[slot][h];
           before += other > mine || (other == mine && h < g);
-          if (h != g && fabsf(other - mine) <= d && mine > -kInf && !by_logit) ++after;
+          after += fabsf(other - mine) <= off + row[h * (per + 1) + per];
         }
+        if (off > 0) --after;  // itself
         stay = before < A.keep;
         close |= after && before + after >= A.keep && before - after < A.keep;
       }

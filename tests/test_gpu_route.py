@@ -339,3 +339,27 @@ def test_gradient_against_differences(torch):
                     f.append(sum(float(q.weights[0, j]) * float(g[0, (r.ids[0] == q.ids[0, j]).nonzero()[0, 0]])
                                  for j in range(3)))
                 assert abs((f[0] - f[1]) / (2 * h) - float(d[0, i])) < 3 * float(g.abs().max()) * (2.0 ** -12 + 2.0 ** -16)
+
+
+CUTS = [(4, 2, 1, 1), (8, 4, 1, 2), (64, 32, 7, 3), (256, 8, 3, 8), (128, 16, 5, 17), (512, 8, 3, 8), (1024, 64, 9, 12)]
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [100.0, 1e4, 1e6])
+@pytest.mark.parametrize("E,groups,keep,k", CUTS)
+def test_biases_that_cancel_in_a_group(torch, scores, size, E, groups, keep, k):
+    """A group's two best have biases of opposite sign, whose sum says nothing about what float32 rounded off them;
+    another group without biases has nearly the same sum, and the cut runs between two such groups."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + groups)
+    T, per, half = 200, E // groups, groups // 2
+    logits = torch.full((T, half, 2, per), -30.0, device="cuda")
+    bias = torch.zeros(half, 2, per, device="cuda")
+    logits[..., :2] = torch.randn(T, half, 1, 2, generator=gen, device="cuda")
+    apart = min(1.0, size * 2.0 ** -23 * (5 if scores == "sigmoid" else 2 * groups))
+    logits[:, :, 1, 1] += apart * torch.randn(T, half, generator=gen, device="cuda")
+    bias[:, 0] = -3 * size
+    bias[:, 0, 0], bias[:, 0, 1] = size, -size
+    at = torch.rand(groups, generator=gen, device="cuda").argsort()
+    logits, bias = logits.view(T, groups, per)[:, at].reshape(T, E), bias.view(groups, per)[at].reshape(E)
+    check(torch, logits, k, f"{scores} {size} {E} in {groups}", bias, scores, groups, keep, 2)
