@@ -338,12 +338,16 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs A, int dtype, bool 
         b1 = fmaxf(b1, fminf(b0, x));
         b0 = fmaxf(b0, x);
       }
+      // of two best, half their sum: below infinity where both are, and minus infinity only without an expert
       const bool two = A.best > 1 && b1 > -kInf;
-      S.g.score[slot][g] = two ? b0 + b1 : b0;
+      const float half = A.best > 1 ? 0.5f : 1.f;
+      b0 *= half;
+      b1 = two ? b1 * half : 0.f;
+      S.g.score[slot][g] = b0 + b1;
       // in the place after the group: how far from its exact sum this score may be, doubled; minus infinity,
       // which no distance is below, for logits and for infinities
-      const float size = fabsf(b0) + (two ? fabsf(b1) : 0.f);
-      row[g * (per + 1) + per] = by_logit || size == kInf ? -kInf : near + 0x1p-22f * size;
+      const float size = fabsf(b0) + fabsf(b1);
+      row[g * (per + 1) + per] = by_logit || size == kInf ? -kInf : half * near + 0x1p-22f * size;
     }
     __syncthreads();
     uint64_t kept = 0;

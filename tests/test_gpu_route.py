@@ -363,3 +363,35 @@ def test_biases_that_cancel_in_a_group(torch, scores, size, E, groups, keep, k):
     at = torch.rand(groups, generator=gen, device="cuda").argsort()
     logits, bias = logits.view(T, groups, per)[:, at].reshape(T, E), bias.view(groups, per)[at].reshape(E)
     check(torch, logits, k, f"{scores} {size} {E} in {groups}", bias, scores, groups, keep, 2)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("E,groups,keep,k", CUTS)
+def test_biases_of_the_largest_size(torch, scores, best, E, groups, keep, k):
+    """The largest finite biases of both signs on none, some and all experts of a group (masks by the type's lowest
+    value among them), beside groups without an expert: sums past float32's range."""
+    most = torch.finfo(torch.float32).max
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(E + best)
+    T, per = 60, E // groups
+    kinds = torch.tensor([most, -most, 0.6 * most, -0.6 * most], device="cuda")
+    for sides in (2, 4):
+        for share in (0.3, 0.7, 1.0):
+            logits = torch.randn(T, groups, per, generator=gen, device="cuda")
+            logits[torch.rand(T, groups, generator=gen, device="cuda") < 0.4] = -math.inf
+            at = torch.randint(0, sides, (groups, 1), generator=gen, device="cuda").expand(-1, per).clone()
+            mixed = torch.rand(groups, per, generator=gen, device="cuda") < 0.2
+            at[mixed] = torch.randint(0, sides, (groups, per), generator=gen, device="cuda")[mixed]
+            large = torch.rand(groups, per, generator=gen, device="cuda") < share
+            bias = torch.where(large, kinds[at], torch.randn(groups, per, generator=gen, device="cuda") * 0.1)
+            check(torch, logits.view(T, E), k, f"{scores} {E} in {groups}, {sides} {share}", bias.view(E), scores, groups,
+                  keep, best)
+    # every expert masked but those of groups that are not there
+    logits = torch.randn(T, groups, per, generator=gen, device="cuda")
+    logits[:, ::2] = -math.inf
+    bias = torch.full((groups, per), -most, device="cuda")
+    bias[::2] = 0.0
+    r = check(torch, logits.view(T, E), min(k, keep * per), f"{scores} {E} in {groups}, lowest", bias.view(E), scores,
+              groups, keep, best)
+    assert bool((r.ids[:, 0] >= 0).all())
