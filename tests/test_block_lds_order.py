@@ -57,3 +57,24 @@ def test_every_barrier_of_the_tiles_waits_for_lds(tmp_path):
     for i in at:
         before = text[i - 1]
         assert re.match(r"s_waitcnt\b", before) and "lgkmcnt(0)" in before, text[i - 4:i + 1]
+
+
+LARGE = """
+#include "%%s/sgmv_fp8_tile.h"
+using namespace sgmv_dev;
+void all_forms(const Fp8Args& A) { fp8_tile_kernel<1, %s, 256, 256, 2, 4, 2, %s><<<1, 512>>>(A); }
+"""
+
+
+@pytest.mark.parametrize("dx", ["false", "true"])
+@pytest.mark.parametrize("near", ["false", "true"])
+def test_every_barrier_of_the_large_tiles_waits_for_all_loads(tmp_path, dx, near):
+    """The same of the tiles of 256 x 256, which hold two stages: the wait before a barrier is for every load as well,
+    those of spilled registers among them, so that these disturb no count."""
+    text = [t.split(";")[0].strip() for t in listing(tmp_path, LARGE % (dx, near)).splitlines()]
+    text = [t for t in text if t and not t.startswith(".")]
+    at = [i for i, t in enumerate(text) if t == "s_barrier"]
+    assert len(at) > 10
+    for i in at:
+        before = text[i - 1]
+        assert re.match(r"s_waitcnt\b", before) and "lgkmcnt(0)" in before and "vmcnt(0)" in before, text[i - 4:i + 1]
