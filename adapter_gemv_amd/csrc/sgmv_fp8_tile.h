@@ -12,8 +12,9 @@
 // 7 * 2^-13 of the sum of the magnitudes, where the rounding to 8 bits was off by up to 2^-4 of each
 // element already.  Block sums are added in float32.
 //
-// Bound: 8192^3 reaches 2050 to 2100 TFLOP/s, the gradient 2310 to 2370, 4096^3 2140 to 2170, MFMAs busy
-// 56 % of the cycles and the clock at 1.7 to 1.9 GHz; the barrier and LDS reads of a stage are the rest.
+// Bound: 8192^3 reaches 2480 TFLOP/s on a card that has been at work (2050 to 2110 in the first 10 ms), its
+// gradient 2440 (2100 to 2370), 4096^3 2240 and 2180.  MFMAs busy 67 % of what the CUs are (SQ_BUSY_CU_CYCLES, 4
+// SIMDs each) and 62 % of the kernel's cycles (GRBM_GUI_ACTIVE); the barrier and LDS reads of a stage are the rest.
 // Ragged groups add the empty half of a group's last tile, and workgroups that wait for the last ones:
 // 1531 x 2 rows over 8 experts of 5120 x 13824, CUs busy 75 %, 328 to 343 us.
 //
@@ -97,7 +98,11 @@ __device__ inline int swizzle(int k) {
 
 // NEAR: the contracted dimension is a multiple of 128, and an offset into the rows, or into a group of
 // W, fits 32 bits: loads are a uniform base and an offset of the lane's, and need no test (8192^3, with
-// a number of stages that is known in rounds: 1822 TFLOP/s to 2020, the gradient 1599 to 2290).
+// a number of stages that is known in rounds: 1822 TFLOP/s to 2020, the gradient 1599 to 2290).  Otherwise
+// the lane's tests and 64-bit offsets do not fit beside the sums of 256 x 256: 31 registers are spilled (29 of
+// DX; NEAR: none, 3 of DX), some read back in every round of stages.  8192 rows, 2880 x 2880, 102 us (1330
+// TFLOP/s), where 2944 x 2944 takes 79 (1800).  Spills count among the loads in flight, but with two buffers
+// every wait is for all of these.
 template <int DT, bool DX, int BR, int BC, int WR, int WC, int BUFS, bool NEAR>
 __global__ __launch_bounds__(64 * WR * WC, BUFS * BR >= 512 && BR < 256 ? 1 : 2) void fp8_tile_kernel(Fp8Args A) {
   using C = Fp8Tile<BR, BC, WR, WC, BUFS>;

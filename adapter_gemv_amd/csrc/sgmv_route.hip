@@ -225,8 +225,11 @@ __device__ __forceinline__ void route_exactly(const RouteArgs& A, int dtype, int
 // stand among a token's first k + 1, or close sums of groups, sigmoids are taken again in 64 bits for
 // these alone (the chosen ones and the next, each in its lane; the two best of each group); a token for
 // which that is not enough, one with NaN, and a softmax, whose sum takes all experts, are done again
-// by route_exactly.  A few of 16384 tokens have such values, and their wavefront is the last to end:
-// 16384 tokens, 256 experts in 8 groups, all redone by route_exactly 25 us, so 18.6; 128 experts, 13.4 and 10.4.
+// by route_exactly.  Of 16384 tokens of float32 logits, 256 experts in 8 groups, 0.1 to 0.3 % have such
+// values, and their wavefront is the last to end: all redone by route_exactly 25 us, so 18.3; 128 experts, 13.4
+// and 10.4.  16-bit logits are often equal: without a bias, but with groups of two best, where the scores
+// choose, 30 % of bfloat16 tokens have equal ones among their first nine: softmax 70 us (float32 25.6), sigmoid
+// 32 (18).
 //
 // Distances: a sigmoid's float32 value is off by at most 2^-22 (its exponential by (|l| + 1) 2^-23 of
 // itself, which the slope s (1 - s) takes to at most 0.48 * 2^-23; sum and reciprocal 2.5 * 2^-24), a
@@ -508,7 +511,8 @@ struct RouteBackArgs {
 
 // L lanes to a token; lane j has its j-th choice.  The row is put together in LDS and written in whole
 // pieces; only a softmax that is not normalised reads all of it.  Bound by that write and the launch:
-// 16384 tokens, 256 experts, float32: 6.9 us, 16.8 MB written; softmax not normalised, 128 experts 10.0.
+// 16384 tokens, 256 experts, float32: 6.9 us, 16.8 MB written.  Softmax not normalised reads the row three times,
+// by single elements, and takes each exponential twice: 128 experts 9.2 to 10.0 us for 16.8 MB.
 template <int DT, bool SIGMOID, int L, int N>
 __global__ __launch_bounds__(64) void route_backward_kernel(RouteBackArgs A, bool normalize, bool vectors) {
   __shared__ __attribute__((aligned(16))) float rows[64 / L][N];
@@ -704,7 +708,7 @@ inline int check_route(int32_t dtype, int32_t n, int32_t E, int32_t k, int32_t s
   if (scores != SGMV_SOFTMAX && scores != SGMV_SIGMOID) return SGMV_ERR_UNSUPPORTED;
   if (n < 0 || E < 1 || k < 1 || k > E) return SGMV_ERR_SHAPE;
   if (E > kMaxGroups || k > kMaxRoutes) return SGMV_ERR_UNSUPPORTED;
-  return n > (1 << 25) ? SGMV_ERR_SHAPE : SGMV_OK;  // n * k fits 31 bits, and 64 threads a row a grid
+  return n > (1 << 25) ? SGMV_ERR_SHAPE : SGMV_OK;  // 64 threads a row fit a grid; n * k may be 2^31: 64 bits
 }
 
 inline int check_combine(int32_t dtype, int32_t n, int32_t k, int32_t h) {

@@ -547,18 +547,21 @@ int sgmv_mx_matmul_quantized(hipStream_t stream, int32_t dtype, void* y, int64_t
  *
  *     weights[t, j] = scale * s[ids[t, j]]           (/ the sum of the chosen s: normalize)
  *
- * Where values are equal the lowest group or expert goes first; the order is that of the exact
- * values, whatever float32 makes of them.  An expert whose l or c is minus infinity is never
- * chosen (a group counts those it has left, and stays only if it has one); places without an
- * expert get the id -1, which belongs to no group, and the weight 0: a padded token is a row of
- * minus infinities.  NaN ranks above all values, and one NaN (softmax: also one plus infinity)
+ * Where values are equal the lowest group or expert goes first.  The order is that of s, c and their
+ * sums as 64-bit floating point has them, whatever float32 makes of them (scores that 64 bits do not
+ * tell apart, sigmoids of 40 and of 50 say, are equal); where nothing is added to a score (no bias, and
+ * all groups kept or group_best 1) it is that of the logits.  An expert whose l or c is minus
+ * infinity is never chosen (a group counts those it has left, and stays only if it has one);
+ * places without an expert get the id -1, which belongs to no group, and the weight 0: a padded
+ * token is a row of minus infinities.  NaN ranks above all values, and one NaN (softmax: also one plus infinity)
  * makes every s of a softmax NaN, or the one s of a sigmoid; weights that depend on it are NaN.
  *   logits   SGMV_F16, SGMV_BF16 or SGMV_F32 [n, n_experts], rows ld_logits elements apart (any
  *            number, not less than n_experts)
  *   bias     float32 [n_experts] or NULL
  *   ids      int32 [n, k] out; weights float32 [n, k] out; both dense
  * 1 <= n_experts <= SGMV_MAX_GROUPS; 1 <= k <= n_experts, at most SGMV_MAX_ROUTES; expert_groups
- * divides n_experts and is at most SGMV_MAX_EXPERT_GROUPS; 1 <= keep_groups <= expert_groups.
+ * divides n_experts and is at most SGMV_MAX_EXPERT_GROUPS; 1 <= keep_groups <= expert_groups; n is at
+ * most 2^25.
  */
 #define SGMV_SOFTMAX 0
 #define SGMV_SIGMOID 1
